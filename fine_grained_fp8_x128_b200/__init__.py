@@ -61,6 +61,7 @@ EXPORTS = (
     "fp8q_moe_dispatch_layout_noalloc",
     "fp8q_quant_act_1x128_ue8m0", "fp8q_quant_w_128x128_ue8m0", "fp8q_gemm_mxf8_ue8m0",
     "fp8q_kernel_clock_counters", "fp8q_quant_act_dual", "fp8q_moe_regroup_order", "fp8q_build_checks",
+    "fp8q_layer_norm", "fp8q_layer_norm_backward_workspace", "fp8q_layer_norm_backward",
 )
 
 _P = ctypes.c_void_p
@@ -107,8 +108,13 @@ _lib.fp8q_quant_act_dual.argtypes = [_P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P,
 _lib.fp8q_quant_act_1x128_ue8m0.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P]
 _lib.fp8q_quant_w_128x128_ue8m0.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P]
 _lib.fp8q_gemm_mxf8_ue8m0.argtypes = [_P, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P]
+_lib.fp8q_layer_norm.argtypes = [_P, ctypes.c_int, _I, _I, _I, _P, _P, ctypes.c_int, ctypes.c_float, _P, _I, _P, _P,
+                                 _P, _I, _P, _I, _P]
+_lib.fp8q_layer_norm_backward_workspace.argtypes = [_I, _I]
+_lib.fp8q_layer_norm_backward.argtypes = [_P, _I, _P, _I, ctypes.c_int, _I, _I, _P, ctypes.c_int, _P, _P, _P, _I, _P,
+                                          _P, _P, _I, _P]
 for _n in EXPORTS[2:]:
-    getattr(_lib, _n).restype = ctypes.c_int
+    getattr(_lib, _n).restype = ctypes.c_int64 if _n.endswith("_workspace") else ctypes.c_int
 
 
 class FP8QError(RuntimeError):
@@ -446,6 +452,96 @@ def fp8q_debug_wait_timeout(budget_cycles: int, stream=None):
     _check(_lib.fp8q_debug_wait_timeout(int(budget_cycles), _stream(stream)), "fp8q_debug_wait_timeout")
 
 
+# ---------------------------------------------------------------- around the projections
+def _dtype(t):
+    """FP8Q_OUT_* of a BF16 or FP32 tensor (FP8Q_OUT_BF16 for None: no elements are read)."""
+    if t is None or t.dtype == torch.bfloat16:
+        return FP8Q_OUT_BF16
+    if t.dtype != torch.float32:
+        raise ValueError(f"expected a bfloat16 or float32 tensor, got {t.dtype}")
+    return FP8Q_OUT_F32
+
+
+def _need(name, t, dtype, shape):
+    """Refuse a given tensor of another type or shape, or not contiguous (None passes)."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _rows(name, t, dtype, shape):
+    """Refuse a given 2D tensor of another type or shape; its rows may lie further apart than they are long."""
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _leading(t):
+    """Row stride of a matrix (0 for None).  With one row or none torch leaves the stride open: any of whole 16-byte
+    units describes it."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2D tensor with a contiguous last dimension")
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _call(name, tensors, args, stream):
+    """Call an entry point on the tensors' device (all of them on one) and its current stream."""
+    given = [t.get_device() for t in tensors if t is not None]
+    device = given[0]
+    if device < 0 or given.count(device) != len(given):
+        raise ValueError(f"{name}: expected CUDA tensors on one device")
+    # the raw handle of the device's current stream: a Stream object would cost a third of a small call's host time
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if device == torch._C._cuda_getDevice():
+        rc = getattr(_lib, name)(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(_lib, name)(*args, handle)
+    if rc != FP8Q_OK:
+        raise FP8QError(rc, name)
+
+
+def fp8q_layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, q=None, sf=None, stream=None):
+    """Rows of x (BF16 or FP32 [M][N]) normalised, times gamma plus beta ([N], BF16 or FP32, or None): into y
+    (x's type), into the 1x128 tiles q uint8 [M][N] with sf float32 [N/128][ld >= M], or both; optional mean and
+    rstd float32 [M]."""
+    M, N = x.shape
+    param = gamma if gamma is not None else beta
+    if param is not None:
+        _need("gamma", gamma, param.dtype, (N,))
+        _need("beta", beta, param.dtype, (N,))
+    _rows("y", y, x.dtype, x.shape)
+    _rows("q", q, torch.uint8, x.shape)
+    _need("mean", mean, torch.float32, (M,))
+    _need("rstd", rstd, torch.float32, (M,))
+    if sf is not None and (sf.dtype != torch.float32 or sf.dim() != 2 or sf.shape[0] != N // 128 or sf.shape[1] < M):
+        raise ValueError("sf: expected float32 [N/128][ld >= M]")
+    _call("fp8q_layer_norm", (x, gamma, beta, y, mean, rstd, q, sf),
+          (_ptr(x), _dtype(x), M, N, _leading(x), _ptr(gamma), _ptr(beta), _dtype(param), eps, _ptr(y), _leading(y),
+           _ptr(mean), _ptr(rstd), _ptr(q), _leading(q), _ptr(sf), _ld(sf) if sf is not None else 0), stream)
+
+
+def fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """Gradients of fp8q_layer_norm: dx (x's type), dgamma and dbeta float32 [N], each optional.  workspace
+    float32, at least fp8q_layer_norm_backward_workspace(M, N) elements, for dgamma and dbeta."""
+    M, N = x.shape
+    _rows("dy", dy, x.dtype, x.shape)
+    _rows("dx", dx, x.dtype, x.shape)
+    if gamma is not None:
+        _need("gamma", gamma, gamma.dtype, (N,))
+    _need("mean", mean, torch.float32, (M,))
+    _need("rstd", rstd, torch.float32, (M,))
+    _need("dgamma", dgamma, torch.float32, (N,))
+    _need("dbeta", dbeta, torch.float32, (N,))
+    if workspace is not None:
+        _need("workspace", workspace, torch.float32, workspace.shape)
+    _call("fp8q_layer_norm_backward", (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace),
+          (_ptr(dy), _leading(dy), _ptr(x), _leading(x), _dtype(x), M, N, _ptr(gamma), _dtype(gamma), _ptr(mean),
+           _ptr(rstd), _ptr(dx), _leading(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+           workspace.numel() if workspace is not None else 0), stream)
+
+
 # ---------------------------------------------------------------- allocation helpers
 def sf_ld(rows: int) -> int:
     """Leading dimension used for [K/128][ld] scale arrays (rows rounded up to 4)."""
@@ -514,3 +610,43 @@ def quant_w_128x128(w, transposed: bool = False, stream=None):
         sft = torch.empty((K // 128, N // 128), dtype=torch.float32, device=w.device)
     fp8q_quant_w_128x128(w, q, sf, qt, sft, stream)
     return (q, sf, qt, sft) if transposed else (q, sf)
+
+
+def _empty_rows(M, N, dtype, device):
+    """[M][N] whose rows lie whole 16-byte units apart."""
+    per = 16 // dtype.itemsize
+    t = torch.empty((M, (N + per - 1) // per * per), dtype=dtype, device=device)
+    return t if N % per == 0 else t[:, :N]
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5, stream=None):
+    """Returns (y of x's type, mean float32 [M], rstd float32 [M])."""
+    M, N = x.shape
+    y = _empty_rows(M, N, x.dtype, x.device)
+    mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    fp8q_layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=stream)
+    return y, mean, rstd
+
+
+def layer_norm_quant(x, gamma=None, beta=None, eps=1e-5, keep_y=False, stream=None):
+    """The norm's 1x128 E4M3 tiles: (q uint8 [M][N], sf float32 [N/128][ld], mean, rstd), and y at the end with keep_y."""
+    M, N = x.shape
+    y = _empty_rows(M, N, x.dtype, x.device) if keep_y else None
+    mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    q = torch.empty((M, N), dtype=torch.uint8, device=x.device)
+    sf = torch.empty((N // 128, sf_ld(M)), dtype=torch.float32, device=x.device)
+    fp8q_layer_norm(x, gamma, beta, eps, y, mean, rstd, q, sf, stream)
+    return (q, sf, mean, rstd, y) if keep_y else (q, sf, mean, rstd)
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
+    """Returns (dx of x's type, dgamma float32 [N], dbeta float32 [N])."""
+    M, N = x.shape
+    dx = _empty_rows(M, N, x.dtype, x.device)
+    dgamma = torch.empty(N, dtype=torch.float32, device=x.device)
+    dbeta = torch.empty(N, dtype=torch.float32, device=x.device)
+    ws = torch.empty(max(1, _lib.fp8q_layer_norm_backward_workspace(M, N)), dtype=torch.float32, device=x.device)
+    fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream)
+    return dx, dgamma, dbeta

@@ -18,6 +18,7 @@
 #include "gemm_pair.cuh"
 #include "gemm_pertensor.cuh"
 #include "mx.cuh"
+#include "norm.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -1206,3 +1207,5 @@ extern "C" fp8q_status fp8q_gemm_mxf8_ue8m0(const void* a, int64_t lda, const ui
   fp8q::gemm_mx_kernel<<<grid, fp8q::kGemmThreads, smem, static_cast<cudaStream_t>(stream)>>>(ta, tb, args);
   return launch_status();
 }
+
+#include "layer_api.cuh"

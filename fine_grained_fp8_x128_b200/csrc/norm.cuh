@@ -1,0 +1,523 @@
+// Layer norm in front of an FP8 projection: forward (into x's type and/or into
+// the projection's 1x128 E4M3 tiles) and backward (input, weight and bias
+// gradients).  Both are HBM-bound streams: each element of the inputs is read
+// once into registers, every sum over a row is formed from registers, and the
+// outputs leave in the same pass.
+//
+//   mu = sum x / N,  v = sum (x - mu)^2 / N,  r = 1 / sqrt(v + eps)
+//   xh = (x - mu) r,  y = xh gamma + beta
+//   backward, g = dy gamma:  dx = r (g - mean(g) - xh mean(g xh))
+//   dgamma = sum_m dy xh,  dbeta = sum_m dy
+//
+// All sums and statistics are FP32.  The variance is the mean square of the
+// deviations (never E[x^2] - mu^2, which cancels when |mu| >> sigma): a warp
+// takes the deviations from its own mean, and the warps' (sum, M2) are joined
+// by the pairwise update of Chan, Golub and LeVeque ("Updating formulae and a
+// pairwise algorithm for computing sample variances", 1979), so that a row
+// needs one block barrier instead of two.
+#pragma once
+
+#include "quant.cuh"
+
+namespace fp8q {
+
+constexpr int kNormMaxN = 16384;       // 1024 threads x 2 vectors of 8 elements
+constexpr int kNormWarpRowMaxN = 512;  // up to here one warp owns a row
+constexpr int kNormWarpRowThreads = 128;
+
+struct LayerNormArgs {
+  const void* x;
+  int64_t M, ldx;
+  int N;
+  const void* gamma;   // may be null: ones
+  const void* beta;    // may be null: zeros
+  float eps;
+  void* y;             // may be null
+  int64_t ldy;
+  float* mean;         // may be null
+  float* rstd;         // may be null
+  uint8_t* q;
+  int64_t ldq;
+  float* sf;
+  int64_t ld_sf;
+};
+
+// Eight consecutive elements as they lie in memory (BF16: one 16-byte word,
+// FP32: two).
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+
+// The first `valid` (0..8) elements from p (16-byte aligned), the rest zero.
+template <typename T, bool kStream>
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* __restrict__ p, int valid) {
+  constexpr int kW = sizeof(T) / 2;
+  if (valid == 8) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(p) + i;
+      r.w[i] = kStream ? __ldcs(src) : __ldg(src);
+    }
+    return;
+  }
+  uint32_t u[4 * kW];
+#pragma unroll
+  for (int i = 0; i < 4 * kW; ++i) u[i] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < valid) {
+      if (sizeof(T) == 4) {
+        u[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+      } else {
+        const uint32_t h = __ldg(reinterpret_cast<const unsigned short*>(p) + j);
+        u[j / 2] |= h << (16 * (j & 1));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kW; ++i) r.w[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&f)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16lo(u[i]);
+    f[2 * i + 1] = bf16hi(u[i]);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&f)[8]) {
+  const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void pack8(Raw8<__nv_bfloat16>& r, const float (&f)[8]) {
+  r.w[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void pack8(Raw8<float>& r, const float (&f)[8]) {
+  r.w[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  r.w[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+}
+
+// The first `valid` elements of r to p; what lies behind them is not touched.
+template <typename T>
+__device__ __forceinline__ void store8(T* __restrict__ p, const Raw8<T>& r, int valid) {
+  constexpr int kW = sizeof(T) / 2;
+  if (valid == 8) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (sizeof(T) == 4) {
+        if (4 * i + k < valid) reinterpret_cast<uint32_t*>(p)[4 * i + k] = u[k];
+      } else {
+        if (2 * k < valid) reinterpret_cast<unsigned short*>(p)[2 * k] = static_cast<unsigned short>(u[k]);
+        if (2 * k + 1 < valid) reinterpret_cast<unsigned short*>(p)[2 * k + 1] = static_cast<unsigned short>(u[k] >> 16);
+      }
+    }
+  }
+}
+
+// gamma or beta (may be null: `none` in every place) of vector v.
+template <typename W>
+__device__ __forceinline__ void load_param8(float (&f)[8], const void* p, int64_t v, int valid, float none) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = none;
+    return;
+  }
+  Raw8<W> r;
+  load8<W, false>(r, static_cast<const W*>(p) + v * 8, valid);
+  unpack8(r, f);
+}
+
+// Sums of two values over the warp: the lower half-warp ends with the total
+// of a, the upper with that of b (one exchange, then four steps within the halves).
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+  const bool up = (lane & 16) != 0;
+  const float give = up ? a : b;
+  float keep = up ? b : a;
+  keep += __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) keep += __shfl_xor_sync(0xFFFFFFFFu, keep, o);
+  return keep;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Four values: lanes 8i .. 8i+7 end with the total of value i.
+__device__ __forceinline__ float warp_sum4(float a, float b, float c, float d, int lane) {
+  const bool up = (lane & 16) != 0;
+  float k0 = up ? c : a, k1 = up ? d : b;
+  k0 += __shfl_xor_sync(0xFFFFFFFFu, up ? a : c, 16);
+  k1 += __shfl_xor_sync(0xFFFFFFFFu, up ? b : d, 16);
+  const bool up2 = (lane & 8) != 0;
+  float k = up2 ? k1 : k0;
+  k += __shfl_xor_sync(0xFFFFFFFFu, up2 ? k0 : k1, 8);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) k += __shfl_xor_sync(0xFFFFFFFFu, k, o);
+  return k;
+}
+
+// Elements of a row that warp `w` of a row group with `warps` warps holds.
+template <int VPT>
+__device__ __forceinline__ int norm_warp_count(int N, int w, int warps) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) n += min(max(N - 256 * (i * warps + w), 0), 256);
+  return n;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  A row group (one warp for N <= 512, else the block) takes two rows
+// at a time: one barrier and one read of gamma and beta serve both, and twice
+// the bytes are in flight.  Thread t holds vectors t, t + nt, ... of eight
+// elements, so 16 consecutive lanes hold one 128-element tile and a tile's
+// maximum is four shuffles.  The tiles quantize y before any rounding to BF16.
+// ---------------------------------------------------------------------------
+template <typename T, typename W, int VPT, bool kWarpRow, bool kTiles>
+__global__ void __launch_bounds__(kWarpRow ? kNormWarpRowThreads : (VPT == 1 ? 512 : 1024))
+layer_norm_kernel(const LayerNormArgs a) {
+  __shared__ float2 part[2][32][2];     // [row-pair parity][warp][row] = (sum, M2)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nt = kWarpRow ? 32 : blockDim.x;
+  const int t = kWarpRow ? lane : threadIdx.x;
+  const int warps = nt >> 5;
+  const int64_t group = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kNormWarpRowThreads / 32) + warp : blockIdx.x;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kWarpRow ? kNormWarpRowThreads / 32 : 1);
+  const int N = a.N;
+  // true divisions by the counts: a row of one value has exactly that mean and no deviations
+  const float n_f = static_cast<float>(N);
+  const float nw_f = static_cast<float>(max(norm_warp_count<VPT>(N, kWarpRow ? 0 : warp, warps), 1));
+  int parity = 0;
+  for (int64_t row0 = group * 2; row0 < a.M; row0 += groups * 2, parity ^= 1) {
+    Raw8<T> raw[2][VPT];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * nt + t;
+        const int valid = row0 + r < a.M ? min(max(N - 8 * v, 0), 8) : 0;
+        load8<T, true>(raw[r][i], static_cast<const T*>(a.x) + (row0 + r) * a.ldx + 8 * static_cast<int64_t>(v), valid);
+      }
+    }
+    // the warp's sums, then its deviations from its own means
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float f[8];
+        unpack8(raw[r][i], f);
+        sum[r] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      }
+    }
+    const float wsum = warp_sum2(sum[0], sum[1], lane);       // this half's row
+    const float wmean = __fdiv_rn(wsum, nw_f);
+    const float mw[2] = {__shfl_sync(0xFFFFFFFFu, wmean, 0), __shfl_sync(0xFFFFFFFFu, wmean, 16)};
+    float m2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float f[8];
+        unpack8(raw[r][i], f);
+        const int valid = min(max(N - 8 * (i * nt + t), 0), 8);
+        if (valid == 8) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = f[j] - mw[r];
+            m2[r] = fmaf(d, d, m2[r]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = j < valid ? f[j] - mw[r] : 0.0f;
+            m2[r] = fmaf(d, d, m2[r]);
+          }
+        }
+      }
+    }
+    const float wm2 = warp_sum2(m2[0], m2[1], lane);
+    float mean_h, m2_h;                                       // of this half-warp's row
+    if (kWarpRow) {
+      mean_h = wmean;
+      m2_h = wm2;
+    } else {
+      if ((lane & 15) == 0) part[parity][warp][lane >> 4] = make_float2(wsum, wm2);
+      __syncthreads();
+      // half-warp h joins row h's warps: lane l takes warps l and l + 16.  The
+      // next pair writes the other buffer, so one barrier a pair is enough.
+      const int h = lane >> 4, w0 = lane & 15, w1 = w0 + 16;
+      const float2 p0 = w0 < warps ? part[parity][w0][h] : make_float2(0.0f, 0.0f);
+      const float2 p1 = w1 < warps ? part[parity][w1][h] : make_float2(0.0f, 0.0f);
+      mean_h = __fdiv_rn(half_warp_sum(p0.x + p1.x), n_f);
+      float s = 0.0f;
+      if (w0 < warps) {
+        const int n0 = norm_warp_count<VPT>(N, w0, warps);
+        const float d = n0 > 0 ? __fdiv_rn(p0.x, static_cast<float>(n0)) - mean_h : 0.0f;
+        s = fmaf(static_cast<float>(n0) * d, d, p0.y);
+      }
+      if (w1 < warps) {
+        const int n1 = norm_warp_count<VPT>(N, w1, warps);
+        const float d = n1 > 0 ? __fdiv_rn(p1.x, static_cast<float>(n1)) - mean_h : 0.0f;
+        s += fmaf(static_cast<float>(n1) * d, d, p1.y);
+      }
+      m2_h = half_warp_sum(s);
+    }
+    const float rstd_h = __frcp_rn(__fsqrt_rn(__fdiv_rn(m2_h, n_f) + a.eps));
+    const float mean[2] = {__shfl_sync(0xFFFFFFFFu, mean_h, 0), __shfl_sync(0xFFFFFFFFu, mean_h, 16)};
+    const float rstd[2] = {__shfl_sync(0xFFFFFFFFu, rstd_h, 0), __shfl_sync(0xFFFFFFFFu, rstd_h, 16)};
+    if (t < 2 && row0 + t < a.M) {
+      if (a.mean != nullptr) a.mean[row0 + t] = t ? mean[1] : mean[0];
+      if (a.rstd != nullptr) a.rstd[row0 + t] = t ? rstd[1] : rstd[0];
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * nt + t;
+      const int valid = min(max(N - 8 * v, 0), 8);
+      float ga[8], be[8];
+      load_param8<W>(ga, a.gamma, v, valid, 1.0f);
+      load_param8<W>(be, a.beta, v, valid, 0.0f);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float f[8];
+        unpack8(raw[r][i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean[r]) * rstd[r], ga[j], be[j]);
+        const bool live = row0 + r < a.M;
+        if (a.y != nullptr && live) {
+          Raw8<T> o;
+          pack8(o, f);
+          store8(static_cast<T*>(a.y) + (row0 + r) * a.ldy + 8 * static_cast<int64_t>(v), o, valid);
+        }
+        if (kTiles) {
+          float m = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+#pragma unroll
+          for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          const float s = tile_scale(m);
+          const float nr = -__frcp_rn(s);
+          // y is an FP32 value here, outside the domain on which the corrected
+          // quotient was shown equal to the IEEE one: it may be one FP32 step
+          // off, which y's own FP32 rounding already is.
+          if (live && valid == 8) {
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = e4m3x2_neg_quot(f[2 * j], f[2 * j + 1], nr, nr, s, s);
+            uint2 o;
+            o.x = (c[0] | (c[1] << 16)) ^ kFlipSigns;
+            o.y = (c[2] | (c[3] << 16)) ^ kFlipSigns;
+            if (chk(8 * static_cast<int64_t>(v) + 7, a.ldq, CHK_Q1))
+              *reinterpret_cast<uint2*>(a.q + (row0 + r) * a.ldq + 8 * static_cast<int64_t>(v)) = o;
+            if ((lane & 15) == 0 && chk(row0 + r, a.ld_sf, CHK_Q1_SF)) a.sf[(v >> 4) * a.ld_sf + row0 + r] = s;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  Row groups as in the forward pass, two rows at a time; mean and
+// rstd come from it.  The two row sums of both rows are one four-value warp
+// reduction and one barrier.  Each thread keeps its columns' dgamma and dbeta
+// in registers over all rows of its block, so the columns cost no further read;
+// a block leaves one partial row of each in the workspace and a second kernel
+// adds the blocks' rows in a fixed order (no atomics: the result does not
+// depend on which block ends first).
+// ---------------------------------------------------------------------------
+struct LayerNormBwdArgs {
+  const void* dy;
+  const void* x;
+  int64_t M, lddy, ldx;
+  int N;
+  const void* gamma;    // may be null: ones
+  const float* mean;
+  const float* rstd;
+  void* dx;             // may be null
+  int64_t lddx;
+  float* partial;       // [gridDim.x][2][N]; null: no weight gradients
+};
+
+template <typename T, typename W, int VPT, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? kNormWarpRowThreads : 1024)
+layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
+  constexpr int kColumns = kWarpRow ? kNormWarpRowMaxN : 1;
+  __shared__ float part[2][32][4];                // [row-pair parity][warp][row 0: g, g xh; row 1: g, g xh]
+  __shared__ float cols[kWarpRow ? kNormWarpRowThreads / 32 : 1][kColumns];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nt = kWarpRow ? 32 : blockDim.x;
+  const int t = kWarpRow ? lane : threadIdx.x;
+  const int warps = nt >> 5;
+  const int64_t group = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kNormWarpRowThreads / 32) + warp : blockIdx.x;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kWarpRow ? kNormWarpRowThreads / 32 : 1);
+  const int N = a.N;
+  const float inv_n = 1.0f / static_cast<float>(N);
+  float dga[VPT][8], dbe[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dga[i][j] = dbe[i][j] = 0.0f;
+  int parity = 0;
+  for (int64_t row0 = group * 2; row0 < a.M; row0 += groups * 2, parity ^= 1) {
+    Raw8<T> rx[2][VPT], rd[2][VPT];
+    float mean[2], rstd[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool live = row0 + r < a.M;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int64_t v = i * nt + t;
+        const int valid = live ? min(max(N - 8 * static_cast<int>(v), 0), 8) : 0;
+        load8<T, true>(rx[r][i], static_cast<const T*>(a.x) + (row0 + r) * a.ldx + 8 * v, valid);
+        load8<T, true>(rd[r][i], static_cast<const T*>(a.dy) + (row0 + r) * a.lddy + 8 * v, valid);
+      }
+      mean[r] = live ? __ldg(a.mean + row0 + r) : 0.0f;
+      rstd[r] = live ? __ldg(a.rstd + row0 + r) : 0.0f;
+    }
+    float s1[2] = {0.0f, 0.0f}, s2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * nt + t;
+      float ga[8];
+      load_param8<W>(ga, a.gamma, v, min(max(N - 8 * v, 0), 8), 1.0f);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float fx[8], fd[8];
+        unpack8(rx[r][i], fx);
+        unpack8(rd[r][i], fd);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {                   // places outside the row have dy = 0
+          const float xh = (fx[j] - mean[r]) * rstd[r];
+          const float g = fd[j] * ga[j];
+          s1[r] += g;
+          s2[r] = fmaf(g, xh, s2[r]);
+          dga[i][j] = fmaf(fd[j], xh, dga[i][j]);
+          dbe[i][j] += fd[j];
+        }
+      }
+    }
+    const float ws = warp_sum4(s1[0], s2[0], s1[1], s2[1], lane);
+    float tot = ws;
+    if (!kWarpRow) {
+      if ((lane & 7) == 0) part[parity][warp][lane >> 3] = ws;
+      __syncthreads();
+      tot = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int w = (lane & 7) + 8 * k;
+        if (w < warps) tot += part[parity][w][lane >> 3];
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, o);
+    }
+    tot *= inv_n;
+    const float c1[2] = {__shfl_sync(0xFFFFFFFFu, tot, 0), __shfl_sync(0xFFFFFFFFu, tot, 16)};
+    const float c2[2] = {__shfl_sync(0xFFFFFFFFu, tot, 8), __shfl_sync(0xFFFFFFFFu, tot, 24)};
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * nt + t;
+        const int valid = min(max(N - 8 * v, 0), 8);
+        float ga[8];
+        load_param8<W>(ga, a.gamma, v, valid, 1.0f);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float fx[8], fd[8];
+          unpack8(rx[r][i], fx);
+          unpack8(rd[r][i], fd);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float xh = (fx[j] - mean[r]) * rstd[r];
+            fd[j] = rstd[r] * (fmaf(fd[j], ga[j], -c1[r]) - xh * c2[r]);
+          }
+          if (row0 + r < a.M) {
+            Raw8<T> o;
+            pack8(o, fd);
+            store8(static_cast<T*>(a.dx) + (row0 + r) * a.lddx + 8 * static_cast<int64_t>(v), o, valid);
+          }
+        }
+      }
+    }
+  }
+  if (a.partial == nullptr) return;
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * N;
+  if constexpr (kWarpRow) {
+    // the block's warps, one after the other per column
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = 8 * (i * 32 + lane) + j;
+          if (c < N) cols[warp][c] = which ? dbe[i][j] : dga[i][j];
+        }
+      __syncthreads();
+      for (int c = threadIdx.x; c < N; c += blockDim.x) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kNormWarpRowThreads / 32; ++w) s += cols[w][c];
+        out[which * N + c] = s;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * nt + t;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (8 * v + j < N) {
+          out[8 * v + j] = dga[i][j];
+          out[N + 8 * v + j] = dbe[i][j];
+        }
+      }
+    }
+  }
+}
+
+// dgamma[c], dbeta[c] <- the sum over `rows` partial rows: 32 columns a block,
+// 32 threads a column, then a fixed tree.
+constexpr int kNormJoinThreads = 1024;
+__global__ void __launch_bounds__(kNormJoinThreads)
+layer_norm_bwd_join_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ dgamma,
+                           float* __restrict__ dbeta) {
+  __shared__ float s[32][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;               // of 2 N columns: dgamma's, then dbeta's
+  float v = 0.0f;
+  if (c < 2 * N)
+    for (int r = ry; r < rows; r += 32) v += partial[static_cast<int64_t>(r) * 2 * N + c];
+  s[ry][cx] = v;
+  __syncthreads();
+  v = s[cx][ry];                                    // warp ry now holds column ry
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const int oc = blockIdx.x * 32 + ry;
+  if (cx == 0 && oc < 2 * N) {
+    if (oc < N) {
+      if (dgamma != nullptr) dgamma[oc] = v;
+    } else if (dbeta != nullptr) {
+      dbeta[oc - N] = v;
+    }
+  }
+}
+
+}  // namespace fp8q

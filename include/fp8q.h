@@ -608,6 +608,55 @@ fp8q_status fp8q_gemm_mxf8_ue8m0(const void* a, int64_t lda, const uint32_t* sfa
                                  void* stream);
 
 /*
+ * Layer norm in front of an FP8 projection or of the MoE layer: one read of x
+ * gives the normalised rows in x's type, the projection's operand in 1x128
+ * E4M3 tiles (the layout fp8q_gemm_blockscaled reads for operand A), or both.
+ *   mu = sum_n x / N;  v = sum_n (x - mu)^2 / N;  r = 1 / sqrt(v + eps)
+ *   y[m,n] = (x[m,n] - mu[m]) * r[m] * gamma[n] + beta[n]
+ * Statistics and y are FP32; the variance is the mean square deviation from
+ * mu.  The tiles quantize the FP32 y (rounded once, to E4M3): s =
+ * max(fl32(amax / 448), fl32(1e-12)), q = e4m3(y / s).  "Fine-Grained FP8
+ * Quantization in DeepSeek", section 2 has the tiles; the pages describe no
+ * norm, so the operator's definition is the formula above.
+ *   x          : [M][ldx] of x_dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32).
+ *   gamma, beta: [N] of param_dtype; NULL stands for ones and zeros.
+ *   y          : optional [M][ldy] of x_dtype.  What lies behind a row's N
+ *                elements is not written.
+ *   mean, rstd : optional FP32 [M] (mu and r), the backward pass's inputs.
+ *   q, sf      : optional, both or neither: E4M3 [M][ldq] and
+ *                sf[(n/128) * ld_sf + m], as fp8q_quant_act_1x128.
+ * Requirements: M >= 0, N >= 1, ldx >= N, eps > 0, y or q given; with y ldy >= N; with
+ * q N % 128 == 0, ldq >= N, ld_sf >= M.  N > 16384 is FP8Q_ERR_UNSUPPORTED.
+ * x, y, gamma, beta, q 16-byte aligned, the rows of x and y whole 16-byte
+ * units apart (ldx, ldy % 8 == 0 for BF16, % 4 == 0 for FP32), ldq % 16 == 0.
+ * N itself may be odd.  M == 0 launches nothing.  One launch.
+ */
+fp8q_status fp8q_layer_norm(const void* x, int x_dtype, int64_t M, int64_t N, int64_t ldx, const void* gamma,
+                            const void* beta, int param_dtype, float eps, void* y, int64_t ldy, float* mean,
+                            float* rstd, void* q, int64_t ldq, float* sf, int64_t ld_sf, void* stream);
+
+/*
+ * Backward pass of fp8q_layer_norm: with xh = (x - mu) r and g = dy * gamma,
+ *   dx     = r * (g - sum_n g / N - xh * sum_n (g xh) / N)
+ *   dgamma = sum_m dy * xh          dbeta = sum_m dy
+ *   dy, x     : [M][lddy], [M][ldx] of x_dtype; mean, rstd: as the forward
+ *               pass wrote them; gamma: as there (NULL stands for ones).
+ *   dx        : optional [M][lddx] of x_dtype.
+ *   dgamma, dbeta : optional FP32 [N], written whole (zeros for M == 0).
+ *   workspace : FP32, at least fp8q_layer_norm_backward_workspace(M, N)
+ *               elements; needed when dgamma or dbeta is given.  Its contents
+ *               need no clearing.  Calls that overlap on the GPU need one each.
+ * Every sum has a fixed order: equal inputs give equal bits.
+ * Requirements: as fp8q_layer_norm; at least one output.  One launch, and a
+ * second for the weight gradients.
+ */
+int64_t fp8q_layer_norm_backward_workspace(int64_t M, int64_t N);
+fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int x_dtype, int64_t M,
+                                     int64_t N, const void* gamma, int param_dtype, const float* mean,
+                                     const float* rstd, void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                                     float* workspace, int64_t workspace_len, void* stream);
+
+/*
  * Clock record of the GEMM kernels.  Every CTA of a GEMM kernel adds, on exit,
  * the SM-clock cycles and the nanoseconds (global timer) it ran; their ratio is
  * the effective SM clock inside those kernels -- under sustained FP8 load the
