@@ -62,6 +62,7 @@ EXPORTS = (
     "fp8q_quant_act_1x128_ue8m0", "fp8q_quant_w_128x128_ue8m0", "fp8q_gemm_mxf8_ue8m0",
     "fp8q_kernel_clock_counters", "fp8q_quant_act_dual", "fp8q_moe_regroup_order", "fp8q_build_checks",
     "fp8q_layer_norm", "fp8q_layer_norm_backward_workspace", "fp8q_layer_norm_backward",
+    "fp8q_moe_few_tokens_workspace", "fp8q_moe_few_tokens",
 )
 
 _P = ctypes.c_void_p
@@ -113,6 +114,9 @@ _lib.fp8q_layer_norm.argtypes = [_P, ctypes.c_int, _I, _I, _I, _P, _P, ctypes.c_
 _lib.fp8q_layer_norm_backward_workspace.argtypes = [_I, _I]
 _lib.fp8q_layer_norm_backward.argtypes = [_P, _I, _P, _I, ctypes.c_int, _I, _I, _P, ctypes.c_int, _P, _P, _P, _I, _P,
                                           _P, _P, _I, _P]
+_lib.fp8q_moe_few_tokens_workspace.argtypes = [_I, _I, _I, _I, _I]
+_lib.fp8q_moe_few_tokens.argtypes = [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _I, ctypes.c_int,
+                                     _P, _I, _P]
 for _n in EXPORTS[2:]:
     getattr(_lib, _n).restype = ctypes.c_int64 if _n.endswith("_workspace") else ctypes.c_int
 
@@ -542,6 +546,32 @@ def fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbe
            workspace.numel() if workspace is not None else 0), stream)
 
 
+def fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, workspace,
+                        stream=None):
+    """y [T][H] (BF16 or FP32) <- the MoE layer of x bf16 [T][H]: expert_ids int32 and expert_weights float32 [T][k];
+    w_gate (or None) and w_up uint8 [E][I][H], w_down uint8 [E][H][I] with float32 128x128 block scales; workspace
+    uint8, fp8q_moe_few_tokens_workspace(T, k, E, H, I) bytes."""
+    T, H = x.shape
+    E, I, _ = w_up.shape
+    k = expert_ids.shape[1]
+    _rows("x", x, torch.bfloat16, (T, H))
+    _need("expert_ids", expert_ids, torch.int32, (T, k))
+    _need("expert_weights", expert_weights, torch.float32, (T, k))
+    _need("w_gate", w_gate, torch.uint8, (E, I, H))
+    _need("w_up", w_up, torch.uint8, (E, I, H))
+    _need("w_down", w_down, torch.uint8, (E, H, I))
+    _need("sf_gate", sf_gate, torch.float32, (E, I // 128, H // 128))
+    _need("sf_up", sf_up, torch.float32, (E, I // 128, H // 128))
+    _need("sf_down", sf_down, torch.float32, (E, H // 128, I // 128))
+    _rows("y", y, y.dtype, (T, H))
+    _need("workspace", workspace, torch.uint8, workspace.shape)
+    _call("fp8q_moe_few_tokens", (x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y,
+                                  workspace),
+          (_ptr(x), T, H, _leading(x), _ptr(expert_ids), _ptr(expert_weights), k, E, _ptr(w_gate), _ptr(sf_gate),
+           _ptr(w_up), _ptr(sf_up), _ptr(w_down), _ptr(sf_down), I, _ptr(y), _leading(y), _dtype(y), _ptr(workspace),
+           workspace.numel()), stream)
+
+
 # ---------------------------------------------------------------- allocation helpers
 def sf_ld(rows: int) -> int:
     """Leading dimension used for [K/128][ld] scale arrays (rows rounded up to 4)."""
@@ -650,3 +680,15 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
     ws = torch.empty(max(1, _lib.fp8q_layer_norm_backward_workspace(M, N)), dtype=torch.float32, device=x.device)
     fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream)
     return dx, dgamma, dbeta
+
+
+def moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down,
+                   out_dtype=torch.bfloat16, stream=None):
+    """The MoE layer for a few tokens (see fp8q_moe_few_tokens); returns y [T][H]."""
+    T, H = x.shape
+    E, I, _ = w_up.shape
+    y = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    n = _lib.fp8q_moe_few_tokens_workspace(T, expert_ids.shape[1], E, H, I)
+    ws = torch.empty(max(1, n), dtype=torch.uint8, device=x.device)
+    fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, ws, stream)
+    return y

@@ -55,6 +55,9 @@ enum : uint32_t {
   CHK_GEMM_SFD = 23,  // GEMM FP8 epilogue scales
   CHK_GROUP = 24,     // grouped GEMM: a tile's rows inside its group and M_total
   CHK_LAYOUT = 25,    // dispatch layout and regroup: row maps
+  CHK_NORM = 26,      // layer norm: rows, statistics, gradients
+  CHK_FEW = 27,       // few-token MoE layer: plan, hidden rows, outputs
+  CHK_LORA = 28,      // adapters: partial sums and outputs
 };
 #ifdef FP8Q_CHECKS
 __device__ __forceinline__ bool chk(int64_t i, int64_t n, uint32_t site) {

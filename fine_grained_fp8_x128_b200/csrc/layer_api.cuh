@@ -67,6 +67,55 @@ void launch_norm_bwd(const fp8q::LayerNormBwdArgs& a, const NormShape& sh, int64
   }
 }
 
+// Dynamic shared memory of a kernel instance, set once per device.
+template <class Kern>
+fp8q_status allow_smem(Kern kern, int bytes, bool* done) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!*done) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    *done = true;
+  }
+  return FP8Q_OK;
+}
+
+template <int MODE, int MT, int G, int S>
+fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  using Sm = fp8q::FewSmem<MT, G, S>;
+  auto kern = fp8q::few_weights_kernel<MODE, MT, G, S>;
+  fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
+  if (st != FP8Q_OK) return st;
+  kern<<<dev->sm_count, fp8q::kFewThreads, Sm::kBytes, s>>>(a);
+  return launch_status();
+}
+
+// G: groups of eight columns (tokens of one expert) a block of work takes.
+template <int G, int S>
+fp8q_status moe_few(const fp8q::FewArgs& a, int y_dtype, DeviceInfo* dev, cudaStream_t s) {
+  fp8q_status st;
+  fp8q::few_plan_kernel<G><<<static_cast<unsigned>(1 + ceil_div(static_cast<int64_t>(a.T) * (a.H / 128), 32)), 1024, 0,
+                             s>>>(a);
+  if ((st = launch_status()) != FP8Q_OK) return st;
+  st = a.wg != nullptr ? launch_few_weights<fp8q::kFewGated, 2, G, S>(a, dev, s)
+                       : launch_few_weights<fp8q::kFewPlain, 2, G, S>(a, dev, s);
+  if (st != FP8Q_OK) return st;
+  const int64_t chunks = a.l.max_positions * (a.I / 128);
+  fp8q::few_hidden_kernel<<<static_cast<unsigned>(grid_for(ceil_div(chunks, fp8q::kFewWarps), dev->sm_count, 8)),
+                            fp8q::kFewThreads, 0, s>>>(a);
+  if ((st = launch_status()) != FP8Q_OK) return st;
+  if ((st = launch_few_weights<fp8q::kFewDown, 2, G, S>(a, dev, s)) != FP8Q_OK) return st;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.H, 1024)), static_cast<unsigned>(a.T));
+  if (y_dtype == FP8Q_OUT_F32) fp8q::few_combine_kernel<float><<<grid, 128, 0, s>>>(a);
+  else fp8q::few_combine_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+  return launch_status();
+}
+
+inline bool few_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  return T <= fp8q::kFewMaxTokens && T * k <= fp8q::kFewMaxEntries && E <= fp8q::kFewMaxExperts && H <= 65536 &&
+         I <= 65536;
+}
+
 }  // namespace
 
 extern "C" {
@@ -161,6 +210,50 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
   fp8q::layer_norm_bwd_join_kernel<<<static_cast<unsigned>(ceil_div(2 * N, 32)), fp8q::kNormJoinThreads, 0, s>>>(
       workspace, static_cast<int>(grid), a.N, dgamma, dbeta);
   return launch_status();
+}
+
+int64_t fp8q_moe_few_tokens_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  if (T <= 0 || k < 1 || k > fp8q::kFewMaxEntries || E < 1 || H < 128 || I < 128 || H % 128 != 0 || I % 128 != 0 ||
+      !few_sizes_ok(T, k, E, H, I))
+    return 0;
+  return fp8q::few_layout(T, k, E, H, I).bytes;
+}
+
+fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* expert_ids,
+                                const float* expert_weights, int64_t k, int64_t E, const void* w_gate,
+                                const float* sf_gate, const void* w_up, const float* sf_up, const void* w_down,
+                                const float* sf_down, int64_t I, void* y, int64_t ldy, int y_dtype, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+  if (T < 0 || k < 1 || k > fp8q::kFewMaxEntries || E < 1 || H < 128 || H % 128 != 0 || I < 128 || I % 128 != 0 ||
+      ldx < H || ldy < H || bad_dtype(y_dtype) || (w_gate == nullptr) != (sf_gate == nullptr))
+    return FP8Q_ERR_INVALID_ARG;
+  if (!few_sizes_ok(T, k, E, H, I)) return FP8Q_ERR_UNSUPPORTED;
+  if (T == 0) return FP8Q_OK;
+  if (x == nullptr || expert_ids == nullptr || expert_weights == nullptr || w_up == nullptr || sf_up == nullptr ||
+      w_down == nullptr || sf_down == nullptr || y == nullptr || workspace == nullptr)
+    return FP8Q_ERR_INVALID_ARG;
+  if (workspace_bytes < fp8q_moe_few_tokens_workspace(T, k, E, H, I)) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(y, 16) || ldy % (16 / elem_size(y_dtype)) != 0 ||
+      !aligned(expert_ids, 4) || !aligned(expert_weights, 4) || !aligned(w_gate, 16) || !aligned(w_up, 16) ||
+      !aligned(w_down, 16) || !aligned(sf_gate, 4) || !aligned(sf_up, 4) || !aligned(sf_down, 4) ||
+      !aligned(workspace, 256))
+    return FP8Q_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  fp8q_status st = device_info(&dev);
+  if (st != FP8Q_OK) return st;
+  fp8q::FewArgs a{};
+  a.x = static_cast<const __nv_bfloat16*>(x); a.ldx = ldx;
+  a.T = static_cast<int>(T); a.k = static_cast<int>(k); a.E = static_cast<int>(E);
+  a.H = static_cast<int>(H); a.I = static_cast<int>(I);
+  a.ids = expert_ids; a.share = expert_weights;
+  a.wg = static_cast<const uint8_t*>(w_gate); a.wu = static_cast<const uint8_t*>(w_up);
+  a.wd = static_cast<const uint8_t*>(w_down);
+  a.sg = sf_gate; a.su = sf_up; a.sd = sf_down;
+  a.y = y; a.ldy = ldy;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.l = fp8q::few_layout(T, k, E, H, I);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return T <= 8 ? moe_few<1, 4>(a, y_dtype, dev, s) : moe_few<2, 3>(a, y_dtype, dev, s);
 }
 
 }  // extern "C"

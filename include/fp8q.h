@@ -657,6 +657,44 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
                                      float* workspace, int64_t workspace_len, void* stream);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens: the decoding form of the
+ * MoE workload's up and down projections, on the weights of
+ * fp8q_grouped_gemm_blockscaled ("FP8 Mixed Precision: DeepSeek-V3 Training
+ * Architecture", section 2: routed experts; section 1: 128x128 weight blocks).
+ *   y[t] = sum_j expert_weights[t,j] * Wd[e] h,  e = expert_ids[t,j]
+ *   h = silu(Wg[e] x[t]) * (Wu[e] x[t]),  silu(v) = v / (1 + exp(-v))
+ *   without a gate matrix: h = Wu[e] x[t]
+ * W[n,k] = decode(code) * its block's scale.  x is taken as it is (BF16, not
+ * quantized) and hidden values as FP16 with a power-of-two scale per 128
+ * (off by at most 2^-11 of the value, or 2^-109 where that is more); products
+ * and sums are FP32.
+ *   x              : BF16 [T][ldx], H wide.
+ *   expert_ids     : device int32 [T][k].  A negative id skips the entry (an
+ *                    expert that lives elsewhere); one >= E skips it and records
+ *                    FP8Q_ERR_INVALID_ARG.  A token may name an expert twice.
+ *                    A token without any entry gets a row of zeros.
+ *   expert_weights : device FP32 [T][k].
+ *   w_gate, w_up   : E4M3 [E][I][H], sf_gate, sf_up: FP32 [E][I/128][H/128];
+ *                    w_gate and sf_gate NULL: no gate.
+ *   w_down         : E4M3 [E][H][I], sf_down: FP32 [E][H/128][I/128].
+ *   y              : [T][ldy] of y_dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32).
+ *   workspace      : fp8q_moe_few_tokens_workspace(T, k, E, H, I) bytes,
+ *                    256-byte aligned.  Its contents need no clearing; calls
+ *                    that overlap on the GPU need one each.
+ * Requirements: T >= 0, k >= 1, E >= 1, H and I multiples of 128, ldx, ldy >=
+ * H; x, y and the weights 16-byte aligned, ldx % 8 == 0, ldy whole 16-byte units.
+ * T > 128, T * k > 1024, E > 1024, H or I > 65536 are FP8Q_ERR_UNSUPPORTED (the
+ * grouped GEMM is the form for more tokens).  T == 0 launches nothing.  Equal
+ * inputs give equal bits.
+ */
+int64_t fp8q_moe_few_tokens_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
+fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* expert_ids,
+                                const float* expert_weights, int64_t k, int64_t E, const void* w_gate,
+                                const float* sf_gate, const void* w_up, const float* sf_up, const void* w_down,
+                                const float* sf_down, int64_t I, void* y, int64_t ldy, int y_dtype, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/*
  * Clock record of the GEMM kernels.  Every CTA of a GEMM kernel adds, on exit,
  * the SM-clock cycles and the nanoseconds (global timer) it ran; their ratio is
  * the effective SM clock inside those kernels -- under sustained FP8 load the

@@ -74,3 +74,60 @@ def layer_norm_backward_bounds(dy, x, gamma, mean, rstd):
     e_dgamma = (dy.abs() * e_xh).sum(0) + (M + 2) * U * (dy * xh).abs().sum(0)
     e_dbeta = M * U * dy.abs().sum(0)
     return e_dx, e_dgamma, e_dbeta
+
+
+# ------------------------------------------------------------------ MoE layer for a few tokens
+def dequant(codes, sf):
+    """float64 weights of E4M3 codes [N][K] and block scales [N/128][K/128]."""
+    w = codes.view(torch.float8_e4m3fn).double()
+    return w * sf.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+
+
+# A 128-wide chunk on the tensor cores: eight instructions of sixteen products,
+# exact ones; each addend is aligned to the step's largest and keeps at least 24
+# bits, so it loses less than 2^-24 of the chunk's sum of magnitudes: 128 2^-24.
+# The scales' two products, the chunks' and the warps' sums: at most 32 FP32
+# roundings of the same magnitudes.
+E_DOT = 2.0 ** -17 + 32 * U
+
+
+def tiny(w):
+    """Where numbers run out of exponents: an FP16 chunk's power of two is at most 2^84, so a value of it is off by up
+    to half of FP16's last step, 2^-25 2^-84 = 2^-109, times its weight; and an FP32 rounding near zero is off by
+    2^-150 where u times the value is less, which the operations of a product and its sums do 2 K + 64 times at most."""
+    return 2.0 ** -109 * w.abs().sum(1) + (2 * w.shape[1] + 64) * 2.0 ** -150
+
+
+def moe_few_tokens(x, ids, share, wg, sg, wu, su, wd, sd):
+    """(y, bound of its error before the last rounding) in float64."""
+    x = x.double()
+    T, H = x.shape
+    y = torch.zeros((T, H), dtype=torch.float64, device=x.device)
+    e_y = torch.zeros_like(y)
+    E = wu.shape[0]
+    for t in range(T):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if e < 0 or e >= E:
+                continue
+            up = dequant(wu[e], su[e])
+            u = up @ x[t]
+            e_u = E_DOT * (up.abs() @ x[t].abs()) + tiny(up)
+            if wg is None:
+                h, e_h = u, e_u
+            else:
+                gate = dequant(wg[e], sg[e])
+                gt = gate @ x[t]
+                e_g = E_DOT * (gate.abs() @ x[t].abs()) + tiny(gate)
+                silu = gt / (1 + torch.exp(-gt))
+                # |silu'| <= 1.1; expf, the sum, the quotient and the product: at most 16 u of h
+                h, e_h = silu * u, 1.1 * e_g * (u.abs() + e_u) + silu.abs() * e_u + 16 * U * (silu * u).abs()
+            # FP16 with a power-of-two scale for 128 values: half a step, or 2^-40 of the chunk's maximum
+            e_h = e_h + 2.0 ** -11 * (h.abs() + e_h)
+            e_h = e_h + 2.0 ** -40 * h.abs().view(-1, 128).amax(1).repeat_interleave(128) + 16 * 2.0 ** -150
+            down = dequant(wd[e], sd[e])
+            w = share[t, j].double()
+            y[t] += w * (down @ h)
+            e_y[t] += w.abs() * (down.abs() @ e_h + (E_DOT + 8 * U * ids.shape[1]) * (down.abs() @ h.abs()) + tiny(down))
+            e_y[t] += 2.0 ** -149
+    return y, e_y

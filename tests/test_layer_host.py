@@ -102,3 +102,52 @@ def test_layer_norm_gradient_against_differences():
     for i in range(N):
         assert abs(difference(gamma, i, lambda t: loss(x, t, beta)) - dgamma[i]) < 1e-7 * (1 + dgamma.abs().max())
         assert abs(difference(beta, i, lambda t: loss(x, gamma, t)) - dbeta[i]) < 1e-7 * (1 + dbeta.abs().max())
+
+
+def test_moe_few_tokens_validation(fp8q):
+    L = fp8q.lib()
+    INV, ALN, UNS = fp8q.FP8Q_ERR_INVALID_ARG, fp8q.FP8Q_ERR_ALIGNMENT, fp8q.FP8Q_ERR_UNSUPPORTED
+    size = L.fp8q_moe_few_tokens_workspace
+    need = size(4, 2, 8, 256, 128)
+    assert need > 0 and size(0, 2, 8, 256, 128) == 0 and size(4, 2, 8, 200, 128) == 0 and size(129, 1, 8, 256, 128) == 0
+    # the hidden rows in FP32 and FP16, every entry's output row: at least these
+    assert need >= 8 * 128 * 6 + 8 * 256 * 4 + 4 * 256 * 2
+
+    def mf(x=FAKE, T=4, H=256, ldx=256, ids=FAKE, share=FAKE, k=2, E=8, wg=FAKE, sg=FAKE, wu=FAKE, su=FAKE, wd=FAKE,
+           sd=FAKE, I=128, y=FAKE, ldy=256, dt=0, ws=FAKE, n=need):
+        return L.fp8q_moe_few_tokens(x, T, H, ldx, ids, share, k, E, wg, sg, wu, su, wd, sd, I, y, ldy, dt, ws, n, None)
+
+    assert mf(T=-1) == INV and mf(k=0) == INV and mf(E=0) == INV and mf(H=200, ldx=256) == INV and mf(I=64) == INV
+    assert mf(H=0) == INV and mf(I=0) == INV and mf(ldx=248) == INV and mf(ldy=248) == INV and mf(dt=3) == INV
+    assert mf(wg=None) == INV and mf(sg=None) == INV                       # one of the pair
+    for name in ("x", "ids", "share", "wu", "su", "wd", "sd", "y", "ws"):
+        assert mf(**{name: None}) == INV
+    assert mf(n=need - 1) == INV
+    assert mf(T=129) == UNS and mf(k=257) == UNS and mf(E=1025) == UNS and mf(I=65664) == UNS
+    assert mf(H=65664, ldx=65664, ldy=65664) == UNS and mf(k=1 << 40) == INV
+    for name in ("x", "wg", "wu", "wd", "y"):
+        assert mf(**{name: FAKE + 8}) == ALN
+    for name in ("ids", "share", "sg", "su", "sd"):
+        assert mf(**{name: FAKE + 2}) == ALN
+    assert mf(ws=FAKE + 128) == ALN and mf(ldx=260) == ALN and mf(ldy=260) == ALN and mf(dt=1, ldy=258) == ALN
+    assert mf(T=0, x=None, ws=None, n=0) == 0
+
+
+def test_moe_few_tokens_binding_refusals(fp8q):
+    x = torch.zeros((2, 256), dtype=torch.bfloat16)
+    ids, share = torch.zeros((2, 1), dtype=torch.int32), torch.zeros((2, 1))
+    w, sf = torch.zeros((3, 128, 256), dtype=torch.uint8), torch.zeros((3, 1, 2))
+    wd, sd = torch.zeros((3, 256, 128), dtype=torch.uint8), torch.zeros((3, 2, 1))
+    call = fp8q.moe_few_tokens
+    with pytest.raises(ValueError, match="CUDA"):
+        call(x, ids, share, w, sf, w, sf, wd, sd)
+    with pytest.raises(ValueError, match="expert_ids"):
+        call(x, ids.long(), share, w, sf, w, sf, wd, sd)
+    with pytest.raises(ValueError, match="x:"):
+        call(x.float(), ids, share, w, sf, w, sf, wd, sd)
+    with pytest.raises(ValueError, match="w_down"):
+        call(x, ids, share, w, sf, w, sf, wd.transpose(1, 2), sd)
+    with pytest.raises(ValueError, match="sf_up"):
+        call(x, ids, share, w, sf, w, sf[:, :, :1], wd, sd)
+    with pytest.raises(ValueError, match="w_gate"):
+        call(x, ids, share, w[:2], sf, w, sf, wd, sd)
