@@ -62,7 +62,7 @@ EXPORTS = (
     "fp8q_quant_act_1x128_ue8m0", "fp8q_quant_w_128x128_ue8m0", "fp8q_gemm_mxf8_ue8m0",
     "fp8q_kernel_clock_counters", "fp8q_quant_act_dual", "fp8q_moe_regroup_order", "fp8q_build_checks",
     "fp8q_layer_norm", "fp8q_layer_norm_backward_workspace", "fp8q_layer_norm_backward",
-    "fp8q_moe_few_tokens_workspace", "fp8q_moe_few_tokens",
+    "fp8q_moe_few_tokens_workspace", "fp8q_moe_few_tokens", "fp8q_lora_apply_workspace", "fp8q_lora_apply",
 )
 
 _P = ctypes.c_void_p
@@ -117,6 +117,9 @@ _lib.fp8q_layer_norm_backward.argtypes = [_P, _I, _P, _I, ctypes.c_int, _I, _I, 
 _lib.fp8q_moe_few_tokens_workspace.argtypes = [_I, _I, _I, _I, _I]
 _lib.fp8q_moe_few_tokens.argtypes = [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _I, ctypes.c_int,
                                      _P, _I, _P]
+_lib.fp8q_lora_apply_workspace.argtypes = [_I, _I, _I, _I]
+_lib.fp8q_lora_apply.argtypes = [_P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _I, ctypes.c_int, _I, _P,
+                                 _I, _P]
 for _n in EXPORTS[2:]:
     getattr(_lib, _n).restype = ctypes.c_int64 if _n.endswith("_workspace") else ctypes.c_int
 
@@ -572,6 +575,30 @@ def fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf
            workspace.numel()), stream)
 
 
+def fp8q_lora_apply(x, rows, group_offsets, a, b, scaling, base, out, workspace, stream=None):
+    """out <- base + scaling[g] * b[g] (a[g] x) for the tokens of each group g: x bf16 [T][K]; rows int32 [T] and
+    group_offsets int32 [groups + 1] (moe_dispatch_layout with k = 1; groups from a.shape[0] on have no adapter);
+    a bf16 [adapters][r][K], b bf16 [adapters][N][r], scaling float32 [adapters] or None; base and out [T][N], BF16 or
+    FP32 (out may be base); workspace float32, fp8q_lora_apply_workspace(T, K, r, groups) elements."""
+    T, K = x.shape
+    n, r, _ = a.shape
+    N = b.shape[1]
+    groups = group_offsets.shape[0] - 1
+    _rows("x", x, torch.bfloat16, x.shape)
+    _need("rows", rows, torch.int32, (T,))
+    _need("group_offsets", group_offsets, torch.int32, (groups + 1,))
+    _need("a", a, torch.bfloat16, (n, r, K))
+    _need("b", b, torch.bfloat16, (n, N, r))
+    _need("scaling", scaling, torch.float32, (n,))
+    _rows("base", base, base.dtype, (T, N))
+    _rows("out", out, base.dtype, (T, N))
+    _need("workspace", workspace, torch.float32, workspace.shape)
+    _call("fp8q_lora_apply", (x, rows, group_offsets, a, b, scaling, base, out, workspace),
+          (_ptr(x), T, K, _leading(x), _ptr(rows), _ptr(group_offsets), groups, _ptr(a), _ptr(b), r, _ptr(scaling), n,
+           _ptr(base), _leading(base), _ptr(out), _leading(out), _dtype(base), N, _ptr(workspace), workspace.numel()),
+          stream)
+
+
 # ---------------------------------------------------------------- allocation helpers
 def sf_ld(rows: int) -> int:
     """Leading dimension used for [K/128][ld] scale arrays (rows rounded up to 4)."""
@@ -692,3 +719,13 @@ def moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, 
     ws = torch.empty(max(1, n), dtype=torch.uint8, device=x.device)
     fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, ws, stream)
     return y
+
+
+def lora_apply(x, rows, group_offsets, a, b, scaling, base, out=None, stream=None):
+    """base plus each token's adapter (see fp8q_lora_apply), into out (allocated when not given); returns out."""
+    if out is None:
+        out = _empty_rows(base.shape[0], base.shape[1], base.dtype, base.device)
+    n = _lib.fp8q_lora_apply_workspace(x.shape[0], x.shape[1], a.shape[1], group_offsets.shape[0] - 1)
+    ws = torch.empty(max(1, n), dtype=torch.float32, device=x.device)
+    fp8q_lora_apply(x, rows, group_offsets, a, b, scaling, base, out, ws, stream)
+    return out

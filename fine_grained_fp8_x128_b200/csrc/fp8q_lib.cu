@@ -17,6 +17,7 @@
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_pertensor.cuh"
+#include "lora.cuh"
 #include "moe_few.cuh"
 #include "mx.cuh"
 #include "norm.cuh"

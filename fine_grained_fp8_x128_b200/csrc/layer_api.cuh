@@ -116,6 +116,64 @@ inline bool few_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) 
          I <= 65536;
 }
 
+// How the adapters' shrink is split: whether the groups hold more than eight
+// tokens on average (blocks of 32 tokens, else of 8), and the K slices that
+// give every SM work when blocks are few.  A function of the sizes alone (the
+// group bounds are on the device).
+struct LoraShape {
+  bool many;
+  int ranks;        // an item's ranks: 16, 32 or 64
+  int64_t blocks;   // at most
+  int slices;
+};
+LoraShape lora_shape(int64_t T, int64_t K, int64_t r, int64_t groups) {
+  LoraShape s;
+  s.many = T > 8 * groups;
+  s.ranks = r <= 16 ? 16 : (r <= 32 ? 32 : 64);
+  const int64_t tile = s.many ? 32 : 8;
+  s.blocks = T / tile + (groups < T ? groups : T);
+  if (s.blocks > T) s.blocks = T;
+  const int64_t items = s.blocks * ceil_div(r, s.ranks);
+  int64_t n = (s.many ? 148 : 2 * 148) / (items < 1 ? 1 : items);
+  const int64_t most = ceil_div(K, 64) / fp8q::kLoraWarps;      // a chunk a warp at least
+  if (n > most) n = most;
+  s.slices = static_cast<int>(n < 1 ? 1 : n);
+  return s;
+}
+
+template <int RT, int G, int P, int S>
+fp8q_status launch_lora_shrink(const fp8q::LoraArgs& a, const LoraShape& sh, DeviceInfo* dev, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  using Sm = fp8q::LoraSmem<RT, G, P, S>;
+  auto kern = fp8q::lora_shrink_kernel<RT, G, P, S>;
+  fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid =
+      grid_for(sh.blocks * ceil_div(a.r, sh.ranks) * a.slices, dev->sm_count, Sm::kBytes <= 100 * 1024 ? 2 : 1);
+  kern<<<static_cast<unsigned>(grid), fp8q::kLoraThreads, Sm::kBytes, s>>>(a);
+  return launch_status();
+}
+
+template <typename T, int KQ, int MB, int CB>
+fp8q_status launch_lora_expand(const fp8q::LoraArgs& a, DeviceInfo* dev, cudaStream_t s) {
+  const int64_t blocks = ceil_div(a.T, 16 * MB) + (a.groups < a.T ? a.groups : a.T);
+  const int64_t grid = grid_for(blocks * ceil_div(a.N, 256 * CB), dev->sm_count, 4);
+  fp8q::lora_expand_kernel<T, KQ, MB, CB><<<static_cast<unsigned>(grid), fp8q::kLoraThreads, 0, s>>>(a);
+  return launch_status();
+}
+template <typename T>
+fp8q_status lora_expand(const fp8q::LoraArgs& a, bool many, DeviceInfo* dev, cudaStream_t s) {
+  if (!many) {
+    if (a.r <= 32) return launch_lora_expand<T, 1, 1, 4>(a, dev, s);
+    if (a.r <= 64) return launch_lora_expand<T, 2, 1, 4>(a, dev, s);
+    return launch_lora_expand<T, 4, 1, 4>(a, dev, s);
+  }
+  constexpr int kMB = sizeof(T) == 4 ? 2 : 4;
+  if (a.r <= 32) return launch_lora_expand<T, 1, kMB, 2>(a, dev, s);
+  if (a.r <= 64) return launch_lora_expand<T, 2, kMB, 2>(a, dev, s);
+  return launch_lora_expand<T, 4, 2, 2>(a, dev, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -254,6 +312,62 @@ fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx
   a.l = fp8q::few_layout(T, k, E, H, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return T <= 8 ? moe_few<1, 4>(a, y_dtype, dev, s) : moe_few<2, 3>(a, y_dtype, dev, s);
+}
+
+int64_t fp8q_lora_apply_workspace(int64_t T, int64_t K, int64_t r, int64_t groups) {
+  if (T <= 0 || K < 8 || K % 8 != 0 || r < 8 || r % 8 != 0 || r > fp8q::kLoraMaxRank || groups < 1 ||
+      groups > fp8q::kLoraMaxGroups)
+    return 0;
+  return lora_shape(T, K, r, groups).slices * T * r;
+}
+
+fp8q_status fp8q_lora_apply(const void* x, int64_t T, int64_t K, int64_t ldx, const int32_t* rows,
+                            const int32_t* group_offsets, int64_t groups, const void* a, const void* b, int64_t r,
+                            const float* scaling, int64_t adapters, const void* base, int64_t ldb, void* out,
+                            int64_t ldo, int dtype, int64_t N, float* workspace, int64_t workspace_len, void* stream) {
+  if (T < 0 || K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0 || r < 8 || r % 8 != 0 || ldx < K || ldb < N || ldo < N ||
+      groups < 1 || adapters < 0 || bad_dtype(dtype))
+    return FP8Q_ERR_INVALID_ARG;
+  if (r > fp8q::kLoraMaxRank || groups > fp8q::kLoraMaxGroups || adapters > 0x7FFFFFFF || T > (1 << 24) ||
+      K > (1 << 24) || N > (1 << 24))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (T == 0) return FP8Q_OK;
+  if (x == nullptr || rows == nullptr || group_offsets == nullptr || base == nullptr || out == nullptr ||
+      workspace == nullptr || (adapters > 0 && (a == nullptr || b == nullptr)))
+    return FP8Q_ERR_INVALID_ARG;
+  if (base == out && ldb != ldo) return FP8Q_ERR_INVALID_ARG;
+  if (workspace_len < fp8q_lora_apply_workspace(T, K, r, groups)) return FP8Q_ERR_INVALID_ARG;
+  const int64_t per16 = 16 / elem_size(dtype);
+  if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || ldb % per16 != 0 ||
+      !aligned(out, 16) || ldo % per16 != 0 || !aligned(rows, 4) || !aligned(group_offsets, 4) || !aligned(scaling, 4) ||
+      !aligned(workspace, 16))
+    return FP8Q_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  fp8q_status st = device_info(&dev);
+  if (st != FP8Q_OK) return st;
+  const LoraShape sh = lora_shape(T, K, r, groups);
+  fp8q::LoraArgs g{};
+  g.x = static_cast<const __nv_bfloat16*>(x); g.T = T; g.ldx = ldx;
+  g.K = static_cast<int>(K); g.N = static_cast<int>(N); g.r = static_cast<int>(r);
+  g.groups = static_cast<int>(groups); g.adapters = static_cast<int>(adapters);
+  g.rows = rows; g.offsets = group_offsets;
+  g.a = static_cast<const __nv_bfloat16*>(a); g.b = static_cast<const __nv_bfloat16*>(b); g.scaling = scaling;
+  g.base = base; g.ldb = ldb; g.out = out; g.ldo = ldo;
+  g.v = workspace; g.slices = sh.slices;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (adapters > 0) {
+    if (sh.many)
+      st = sh.ranks == 16   ? launch_lora_shrink<1, 4, 1, 4>(g, sh, dev, s)
+           : sh.ranks == 32 ? launch_lora_shrink<2, 4, 1, 4>(g, sh, dev, s)
+                            : launch_lora_shrink<4, 4, 1, 3>(g, sh, dev, s);
+    else
+      st = sh.ranks == 16   ? launch_lora_shrink<1, 1, 2, 4>(g, sh, dev, s)
+           : sh.ranks == 32 ? launch_lora_shrink<2, 1, 2, 4>(g, sh, dev, s)
+                            : launch_lora_shrink<4, 1, 2, 2>(g, sh, dev, s);
+    if (st != FP8Q_OK) return st;
+  }
+  return dtype == FP8Q_OUT_F32 ? lora_expand<float>(g, sh.many, dev, s)
+                               : lora_expand<__nv_bfloat16>(g, sh.many, dev, s);
 }
 
 }  // extern "C"

@@ -695,6 +695,44 @@ fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx
                                 int64_t workspace_bytes, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection: the tokens of
+ * a batch share one projection (fp8q_gemm_blockscaled wrote its output, base)
+ * and each adds its own adapter's product.
+ *   out[t] = base[t] + scaling[a] * B[a] (A[a] x[t]),  a = the adapter of token t
+ * The pages describe no adapters; the operator's definition is the formula.
+ *   x             : BF16 [T][ldx], K wide (not quantized).
+ *   rows, group_offsets : the tokens by group, as fp8q_moe_dispatch_layout
+ *                   writes them with a token's adapter as its expert and k = 1:
+ *                   group g's tokens are rows[group_offsets[g]] ..
+ *                   rows[group_offsets[g+1] - 1]; device int32 [T] and [groups + 1].
+ *                   Group g uses adapter g; groups at or above `adapters` have
+ *                   none (out = base).  A token is in one group at most; a token
+ *                   in none keeps its row of out as it was.  Offsets that
+ *                   decrease or leave [0, T], and rows outside [0, T) (skipped),
+ *                   record FP8Q_ERR_INVALID_ARG in the device status word.
+ *   a, b          : BF16 [adapters][r][K] and [adapters][N][r], packed.
+ *   scaling       : optional device FP32 [adapters]; NULL stands for ones.
+ *   base, out     : [T][ldb], [T][ldo] of dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32),
+ *                   N wide; out may be base itself (then ldo == ldb).
+ *   workspace     : FP32, at least fp8q_lora_apply_workspace(T, K, r, groups)
+ *                   elements, 16-byte aligned; no clearing needed; calls that
+ *                   overlap on the GPU need one each.
+ * Products and sums are FP32; A x enters B's product in BF16 parts that
+ * keep it to 2^-16 of itself (BF16 output) or 2^-24 (FP32).  One rounding to
+ * the output.
+ * Requirements: T >= 0, groups >= 1; K, N, r multiples of 8, at least 8; ldx >= K, ldb
+ * and ldo >= N; x, a, b, base, out 16-byte aligned, ldx % 8 == 0, ldb and ldo
+ * whole 16-byte units.  r > 128, groups > 1024, T, K or N > 2^24 are
+ * FP8Q_ERR_UNSUPPORTED.  T == 0 launches nothing.  Two launches.  Equal inputs
+ * give equal bits.
+ */
+int64_t fp8q_lora_apply_workspace(int64_t T, int64_t K, int64_t r, int64_t groups);
+fp8q_status fp8q_lora_apply(const void* x, int64_t T, int64_t K, int64_t ldx, const int32_t* rows,
+                            const int32_t* group_offsets, int64_t groups, const void* a, const void* b, int64_t r,
+                            const float* scaling, int64_t adapters, const void* base, int64_t ldb, void* out,
+                            int64_t ldo, int dtype, int64_t N, float* workspace, int64_t workspace_len, void* stream);
+
+/*
  * Clock record of the GEMM kernels.  Every CTA of a GEMM kernel adds, on exit,
  * the SM-clock cycles and the nanoseconds (global timer) it ran; their ratio is
  * the effective SM clock inside those kernels -- under sustained FP8 load the

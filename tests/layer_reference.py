@@ -131,3 +131,26 @@ def moe_few_tokens(x, ids, share, wg, sg, wu, su, wd, sd):
             e_y[t] += w.abs() * (down.abs() @ e_h + (E_DOT + 8 * U * ids.shape[1]) * (down.abs() @ h.abs()) + tiny(down))
             e_y[t] += 2.0 ** -149
     return y, e_y
+
+
+# ------------------------------------------------------------------ low-rank adapters
+def lora(x, ids, a, b, scaling, base):
+    """(out, bound of its error before the last rounding) in float64; ids outside [0, adapters): none."""
+    out, e = base.double(), torch.zeros(base.shape, dtype=torch.float64, device=base.device)
+    parts = 3 if base.dtype == torch.float32 else 2
+    for i in range(a.shape[0]):
+        t = torch.nonzero(ids == i)[:, 0]
+        if not len(t):
+            continue
+        s = 1.0 if scaling is None else scaling[i].double()
+        A, B, xt = a[i].double(), b[i].double(), x[t].double()
+        v = s * (xt @ A.t())
+        mag = abs(s) * (xt.abs() @ A.abs().t())
+        # a chunk of 64 elements on the tensor cores (64 addends, each losing under 2^-24 of their sum), then at most
+        # 64 FP32 additions; the product with s; the BF16 parts
+        e_v = (64 + 64 + 1) * U * mag + 2.0 ** (-8 * parts) * v.abs()
+        out[t] += v @ B.t()
+        vb = v.abs() @ B.abs().t()
+        # parts * r addends on the tensor cores (the parts' magnitudes together at most 1 + 2^-7 of v's)
+        e[t] += e_v @ B.abs().t() * (1 + 2.0 ** -7) + parts * B.shape[1] * U * (1 + 2.0 ** -6) * vb
+    return out, e + U * out.abs()

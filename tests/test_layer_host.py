@@ -151,3 +151,54 @@ def test_moe_few_tokens_binding_refusals(fp8q):
         call(x, ids, share, w, sf, w, sf[:, :, :1], wd, sd)
     with pytest.raises(ValueError, match="w_gate"):
         call(x, ids, share, w[:2], sf, w, sf, wd, sd)
+
+
+def test_lora_validation(fp8q):
+    L = fp8q.lib()
+    INV, ALN, UNS = fp8q.FP8Q_ERR_INVALID_ARG, fp8q.FP8Q_ERR_ALIGNMENT, fp8q.FP8Q_ERR_UNSUPPORTED
+    size = L.fp8q_lora_apply_workspace
+    need = size(40, 256, 16, 3)
+    assert need >= 40 * 16 and size(0, 256, 16, 3) == 0 and size(40, 255, 16, 3) == 0 and size(40, 256, 136, 3) == 0
+    assert size(40, 256, 16, 1025) == 0
+    # few blocks: the K slices' partial sums lie side by side
+    assert size(1, 7168, 16, 1) % 16 == 0 and size(1, 7168, 16, 1) > 16 and size(4096, 7168, 64, 1) == 4096 * 64
+
+    def lo(x=FAKE, T=40, K=256, ldx=256, rows=FAKE, off=FAKE, groups=3, a=FAKE, b=FAKE, r=16, s=FAKE, n=2, base=FAKE,
+           ldb=512, out=2 * FAKE, ldo=512, dt=0, N=512, ws=FAKE, wl=need):
+        return L.fp8q_lora_apply(x, T, K, ldx, rows, off, groups, a, b, r, s, n, base, ldb, out, ldo, dt, N, ws, wl, None)
+
+    assert lo(T=-1) == INV and lo(K=252) == INV and lo(K=0) == INV and lo(N=508) == INV and lo(r=12) == INV
+    assert lo(r=0) == INV and lo(ldx=248) == INV and lo(ldb=504) == INV and lo(ldo=504) == INV
+    assert lo(groups=0) == INV and lo(n=-1) == INV and lo(dt=2) == INV
+    for name in ("x", "rows", "off", "a", "b", "base", "out", "ws"):
+        assert lo(**{name: None}) == INV
+    assert lo(wl=need - 1) == INV and lo(out=FAKE, ldo=520) == INV       # in place needs the same rows
+    assert lo(r=136) == UNS and lo(groups=1025) == UNS and lo(T=(1 << 24) + 1) == UNS
+    for name in ("x", "a", "b", "base", "ws"):
+        assert lo(**{name: FAKE + 8}) == ALN
+    for name in ("rows", "off", "s"):
+        assert lo(**{name: FAKE + 2}) == ALN
+    assert lo(out=2 * FAKE + 8) == ALN and lo(ldx=260) == ALN and lo(ldb=516) == ALN and lo(ldo=516) == ALN
+    assert lo(dt=1, ldb=514) == ALN
+    assert lo(T=0, x=None, out=None, ws=None, wl=0) == 0
+
+
+def test_lora_binding_refusals(fp8q):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    a, b = torch.zeros((2, 16, 64), dtype=torch.bfloat16), torch.zeros((2, 32, 16), dtype=torch.bfloat16)
+    rows, off = torch.zeros(4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    base = torch.zeros((4, 32), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        fp8q.lora_apply(x, rows, off, a, b, None, base)
+    with pytest.raises(ValueError, match="rows"):
+        fp8q.lora_apply(x, rows.long(), off, a, b, None, base)
+    with pytest.raises(ValueError, match="a:"):
+        fp8q.lora_apply(x, rows, off, a.float(), b, None, base)
+    with pytest.raises(ValueError, match="b:"):
+        fp8q.lora_apply(x, rows, off, a, b[:, :, :8], None, base)
+    with pytest.raises(ValueError, match="scaling"):
+        fp8q.lora_apply(x, rows, off, a, b, torch.ones(3), base)
+    with pytest.raises(ValueError, match="base"):
+        fp8q.lora_apply(x, rows, off, a, b, None, base[:, :24])
+    with pytest.raises(ValueError, match="out"):
+        fp8q.lora_apply(x, rows, off, a, b, None, base, out=base.float())
