@@ -79,36 +79,61 @@ fp8q_status allow_smem(Kern kern, int bytes, bool* done) {
   return FP8Q_OK;
 }
 
-template <int MODE, int MT, int G, int S>
+// Launch that may start while the kernel before it in the stream runs out; the
+// kernel itself waits for that one's end (griddepcontrol.wait) before any access.
+template <class Kern, class... Args>
+fp8q_status launch_after(Kern kern, dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8Q_ERR_CUDA;
+  }
+  return FP8Q_OK;
+}
+
+template <int MODE, int RT, int G, int S>
 fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  using Sm = fp8q::FewSmem<MT, G, S>;
-  auto kern = fp8q::few_weights_kernel<MODE, MT, G, S>;
+  using Sm = fp8q::FewSmem<RT, G, S>;
+  auto kern = fp8q::few_weights_kernel<MODE, RT, G, S>;
   fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
   if (st != FP8Q_OK) return st;
-  kern<<<dev->sm_count, fp8q::kFewThreads, Sm::kBytes, s>>>(a);
-  return launch_status();
+  const int64_t K = MODE == fp8q::kFewDown ? a.I : a.H, rows = static_cast<int64_t>(a.E) * (MODE == fp8q::kFewDown ? a.H : a.I);
+  const uint8_t* lo = MODE == fp8q::kFewDown ? a.wd : (MODE == fp8q::kFewGated ? a.wg : a.wu);
+  CUtensorMap map_lo, map_hi;
+  if ((st = make_tmap(&map_lo, lo, K, rows, K, MODE == fp8q::kFewGated ? 8 * RT : 16 * RT)) != FP8Q_OK) return st;
+  map_hi = map_lo;
+  if (MODE == fp8q::kFewGated && (st = make_tmap(&map_hi, a.wu, K, rows, K, 8 * RT)) != FP8Q_OK) return st;
+  return launch_after(kern, dim3(dev->sm_count), fp8q::kFewWeightThreads, Sm::kBytes, s, map_lo, map_hi, a);
 }
 
 // G: groups of eight columns (tokens of one expert) a block of work takes.
-template <int G, int S>
+template <int RT, int G, int S>
 fp8q_status moe_few(const fp8q::FewArgs& a, int y_dtype, DeviceInfo* dev, cudaStream_t s) {
   fp8q_status st;
   fp8q::few_plan_kernel<G><<<static_cast<unsigned>(1 + ceil_div(static_cast<int64_t>(a.T) * (a.H / 128), 32)), 1024, 0,
                              s>>>(a);
   if ((st = launch_status()) != FP8Q_OK) return st;
-  st = a.wg != nullptr ? launch_few_weights<fp8q::kFewGated, 2, G, S>(a, dev, s)
-                       : launch_few_weights<fp8q::kFewPlain, 2, G, S>(a, dev, s);
+  st = a.wg != nullptr ? launch_few_weights<fp8q::kFewGated, RT, G, S>(a, dev, s)
+                       : launch_few_weights<fp8q::kFewPlain, RT, G, S>(a, dev, s);
   if (st != FP8Q_OK) return st;
   const int64_t chunks = a.l.max_positions * (a.I / 128);
-  fp8q::few_hidden_kernel<<<static_cast<unsigned>(grid_for(ceil_div(chunks, fp8q::kFewWarps), dev->sm_count, 8)),
-                            fp8q::kFewThreads, 0, s>>>(a);
-  if ((st = launch_status()) != FP8Q_OK) return st;
-  if ((st = launch_few_weights<fp8q::kFewDown, 2, G, S>(a, dev, s)) != FP8Q_OK) return st;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.H, 1024)), static_cast<unsigned>(a.T));
-  if (y_dtype == FP8Q_OUT_F32) fp8q::few_combine_kernel<float><<<grid, 128, 0, s>>>(a);
-  else fp8q::few_combine_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
-  return launch_status();
+  const int64_t grid = grid_for(ceil_div(chunks, fp8q::kFewThreads / 32), dev->sm_count, 8);
+  st = launch_after(fp8q::few_hidden_kernel, dim3(static_cast<unsigned>(grid)), fp8q::kFewThreads, 0, s, a);
+  if (st != FP8Q_OK) return st;
+  if ((st = launch_few_weights<fp8q::kFewDown, RT, G, S>(a, dev, s)) != FP8Q_OK) return st;
+  const dim3 cg(static_cast<unsigned>(ceil_div(a.H, 1024)), static_cast<unsigned>(a.T));
+  return y_dtype == FP8Q_OUT_F32 ? launch_after(fp8q::few_combine_kernel<float>, cg, 128, 0, s, a)
+                                 : launch_after(fp8q::few_combine_kernel<__nv_bfloat16>, cg, 128, 0, s, a);
 }
 
 inline bool few_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
@@ -311,7 +336,7 @@ fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx
   a.ws = static_cast<uint8_t*>(workspace);
   a.l = fp8q::few_layout(T, k, E, H, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return T <= 8 ? moe_few<1, 4>(a, y_dtype, dev, s) : moe_few<2, 3>(a, y_dtype, dev, s);
+  return T <= 8 ? moe_few<2, 1, 4>(a, y_dtype, dev, s) : moe_few<4, 2, 4>(a, y_dtype, dev, s);
 }
 
 int64_t fp8q_lora_apply_workspace(int64_t T, int64_t K, int64_t r, int64_t groups) {

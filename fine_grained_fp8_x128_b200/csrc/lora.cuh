@@ -108,6 +108,9 @@ __device__ __forceinline__ int64_t lora_token(const LoraArgs& a, int pos) {
   return t;
 }
 
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(live ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -119,9 +122,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // ---------------------------------------------------------------------------
 // Shrink.  An item is a block of up to 8 G tokens of one adapter times up to
 // 16 RT of its ranks times one K slice; the block's warps split the slice's
-// chunks of 32 P elements and join their FP32 sums in shared memory.  Operands
-// in fragment order and a barrier-free ring of S units a warp, as in the MoE
-// weight passes.
+// chunks of 32 P elements and join their FP32 sums in shared memory.  The
+// operands' order along K is free as long as both share it: lane (g, t) takes
+// the 16-byte piece t of a chunk of rows g and g + 8, in fragment order.  Every lane
+// reads back only what it copied itself (cp.async), so the ring of S units (one
+// unit: one chunk of one item) needs no barrier, and runs on across items.
 // ---------------------------------------------------------------------------
 template <int RT, int G, int P, int S>
 struct LoraSmem {

@@ -14,15 +14,17 @@
 // shared memory to be a tcgen05 operand, twice the bytes that came in, and at
 // these token counts the matrix instructions are far from their limit.
 //
-// Five launches:
-//   plan     tokens by expert in blocks of 8 G columns; x to FP16 chunks
+// Five launches, each started while the one before runs out (programmatic
+// dependent launch) and waiting for its end before any access:
+//   plan     tokens by expert in blocks of 8 G columns; x to FP16 records
 //   up       hidden rows, FP32
-//   hidden   hidden rows to FP16 chunks
+//   hidden   hidden rows to FP16 records
 //   down     each (token, slot)'s output row, FP32
 //   combine  the weighted sum over a token's slots, in slot order
 // No atomic touches a result: equal inputs give equal bits.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "norm.cuh"
@@ -32,8 +34,11 @@ namespace fp8q {
 constexpr int kFewMaxTokens = 128;
 constexpr int kFewMaxEntries = 1024;
 constexpr int kFewMaxExperts = 1024;
-constexpr int kFewThreads = 256;
-constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewThreads = 256;              // hidden
+constexpr int kFewWarps = 8;                  // of a weight pass, which multiply
+constexpr int kFewWeightThreads = 32 * (kFewWarps + 2);   // and two that load
+constexpr int kFewTiles = 2;                  // row tiles a multiplying warp takes
+constexpr int kFewRecord = 272;               // a chunk's 128 FP16 values and its scale, 16-byte units
 
 // What the plan leaves for the other launches.  Positions number the entries
 // (token, slot) expert by expert, each expert's first position a multiple of 8.
@@ -51,11 +56,10 @@ struct FewPlan {
 struct FewLayout {
   int64_t max_blocks, max_positions;
   int64_t block_expert, block_start, block_count, entry;
-  int64_t xh, xs;       // FP16 [T][H], FP32 [H/128][ld_xs]
+  int64_t xr;           // records [T][H/128]
   int64_t hid;          // FP32 [max_positions][I]
-  int64_t hh, hs;       // FP16 [max_positions][I], FP32 [I/128][max_positions]
+  int64_t hr;           // records [max_positions][I/128]
   int64_t yp;           // FP32 [T k][H]
-  int64_t ld_xs;
   int64_t bytes;
 };
 __host__ __device__ inline int64_t few_align(int64_t v) { return (v + 255) / 256 * 256; }
@@ -65,17 +69,14 @@ __host__ __device__ inline FewLayout few_layout(int64_t T, int64_t k, int64_t E,
   const int64_t groups = n < E ? n : E;
   l.max_positions = (n + 7 * groups + 7) / 8 * 8;
   l.max_blocks = l.max_positions / 8;
-  l.ld_xs = (T + 3) / 4 * 4;
   int64_t o = few_align(sizeof(FewPlan));
   l.block_expert = o; o = few_align(o + 4 * l.max_blocks);
   l.block_start = o; o = few_align(o + 4 * l.max_blocks);
   l.block_count = o; o = few_align(o + 4 * l.max_blocks);
   l.entry = o; o = few_align(o + 4 * l.max_positions);
-  l.xh = o; o = few_align(o + 2 * T * H);
-  l.xs = o; o = few_align(o + 4 * (H / 128) * l.ld_xs);
+  l.xr = o; o = few_align(o + kFewRecord * T * (H / 128));
   l.hid = o; o = few_align(o + 4 * l.max_positions * I);
-  l.hh = o; o = few_align(o + 2 * l.max_positions * I);
-  l.hs = o; o = few_align(o + 4 * (I / 128) * l.max_positions);
+  l.hr = o; o = few_align(o + kFewRecord * l.max_positions * (I / 128));
   l.yp = o; o = few_align(o + 4 * n * H);
   l.bytes = o;
   return l;
@@ -99,17 +100,23 @@ __device__ __forceinline__ const FewPlan* few_plan(const FewArgs& a) { return re
 template <typename T>
 __device__ __forceinline__ T* few_at(const FewArgs& a, int64_t off) { return reinterpret_cast<T*>(a.ws + off); }
 
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
-// FP16 chunks: 128 values times a power of two that takes their largest
-// magnitude into [2^14, 2^15).  The scaling is exact, FP16 keeps 11 bits (a
-// BF16 value has 8, so x is exact) down to 2^-28 of the chunk's maximum, and
-// what lies below is off by at most 2^-40 of that maximum, under the FP32
-// accumulation's own rounding.  A hidden value is off by at most 2^-11 of itself.
-// The power is at most 2^84, so that its inverse times a block scale (>= 1e-12)
-// is a normal FP32 number: a chunk under 2^-98 loses bits, 2^-109 at most.
+// FP16 records: 128 values times a power of two that takes their largest
+// magnitude into [2^14, 2^15), and the inverse power.  The scaling is exact, FP16
+// keeps 11 bits (a BF16 value has 8, so x is exact) down to 2^-28 of the
+// chunk's maximum, and what lies below is off by at most 2^-40 of that maximum,
+// under the FP32 accumulation's own rounding.  A hidden value is off by at most
+// 2^-11 of itself.  The power is at most 2^84, so that its inverse times a block
+// scale (>= 1e-12) is a normal FP32 number: a chunk under 2^-98 loses bits,
+// 2^-109 at most.
+// Value k = 32 t + 8 q + i lies at 16-byte unit 4 q + t, place i: the order in
+// which lanes t of a warp read their multiplier operand, without bank conflicts.
 // A warp owns one chunk, four consecutive values a lane.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void few_chunk(const float (&f)[4], __half* dst, float* scale, int lane) {
+__device__ __forceinline__ void few_record(const float (&f)[4], uint8_t* dst, int lane) {
   float m = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -120,8 +127,9 @@ __device__ __forceinline__ void few_chunk(const float (&f)[4], __half* dst, floa
   uint2 o;
   o.x = *reinterpret_cast<const uint32_t*>(&h0);
   o.y = *reinterpret_cast<const uint32_t*>(&h1);
-  *reinterpret_cast<uint2*>(dst + 4 * lane) = o;
-  if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+  const int t = lane >> 3, q = (lane & 7) >> 1;
+  *reinterpret_cast<uint2*>(dst + (4 * q + t) * 16 + 8 * (lane & 1)) = o;
+  if (lane == 0) *reinterpret_cast<float*>(dst + 256) = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 }
 
 // Inclusive scan of two counters over 1024 threads.
@@ -152,6 +160,7 @@ __device__ __forceinline__ int2 few_scan(int2 v, int2 (&sums)[32]) {
 template <int G>
 __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
   const int tid = threadIdx.x, lane = tid & 31;
+  pdl_launch();
   if (blockIdx.x > 0) {
     const int chunks = a.H / 128;
     const int item = (blockIdx.x - 1) * 32 + (tid >> 5);
@@ -159,8 +168,7 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
     const int t = item / chunks, kb = item - t * chunks;
     const uint2 r = *reinterpret_cast<const uint2*>(a.x + t * a.ldx + kb * 128 + 4 * lane);
     const float f[4] = {bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y)};
-    few_chunk(f, few_at<__half>(a, a.l.xh) + static_cast<int64_t>(t) * a.H + kb * 128,
-              few_at<float>(a, a.l.xs) + kb * a.l.ld_xs + t, lane);
+    few_record(f, few_at<uint8_t>(a, a.l.xr) + static_cast<int64_t>(item) * kFewRecord, lane);
     return;
   }
   __shared__ int count[kFewMaxExperts], start[kFewMaxExperts];
@@ -208,27 +216,29 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The two weight passes.  An item is MT tiles of 16 weight rows of one expert
-// times one block of up to 8 G of its columns; the block's eight warps split
-// the 128-wide K chunks (warp w: chunks w, w + 8, ...), which keeps 1 KB of a row
-// together in time, and their FP32 sums are joined in shared memory in warp order.
+// The two weight passes.  An item is RT tiles of 16 weight rows of one expert
+// times one block of up to 8 G of its columns.  A block's 8 multiplying warps
+// take an item in stages of KC 128-wide K chunks, RT KC = 16: a warp multiplies two
+// tiles by one chunk of the stage, so that the columns' operands and a stage's
+// bookkeeping serve 4 KB of codes, and the warps' FP32 sums are joined once an
+// item, in chunk order.  (Sixteen warps of one tile each were bound by their
+// instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, where
+// the loads alone take 43.)
+// Two more warps keep the ring of S stages full, across items: TMA boxes of
+// rows x 128 bytes for the codes (half of the boxes each: one lane issues a
+// box in some 75 clocks), one bulk copy a column for its KC records, and the
+// stage's block scales, which start on no 16-byte boundary and so are per-thread
+// copies that arrive on the stage's barrier.  They look up an item's block and
+// columns while they load the item before, and hand it on with the stage.
 //
-// A tile's operand order is free along K as long as both operands share it, so
-// lane (g, t) of a warp takes bytes 16 t .. and 64 + 16 t .. of rows g and g + 8:
-// 16-byte loads straight into fragment order.  Every lane reads back only what
-// it copied itself (cp.async, 512 contiguous bytes a warp instruction), so the
-// ring of S units (one unit: one chunk of one item) needs no barrier, and runs on
-// across items: the next item's weights are in flight while this one is joined.
-// Only the few scales of a unit are shared by the lanes.
+// Along K an instruction's operands may be taken in any order that both share:
+// lane (g, t) takes bytes 32 t .. 32 t + 31 of rows g and g + 8, which under the
+// TMA's 128-byte swizzle are two conflict-free 16-byte reads a row.
+// Columns past the block's count hold what the ring held before: a column's
+// garbage stays in that column, and is not stored.
 // ---------------------------------------------------------------------------
 enum : int { kFewGated = 0, kFewPlain = 1, kFewDown = 2 };
 
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4_or_zero(uint32_t smem, const void* gmem, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(gmem), "r"(live ? 4 : 0) : "memory");
-}
 // Four E4M3 codes (element order) -> two FP16 pairs; exact.
 __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
@@ -243,215 +253,262 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// A four-byte asynchronous copy, and this lane's arrival once its copies so far are done.
+__device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// The multiplying warps' own barrier.
+__device__ __forceinline__ void few_join_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+}
 
-template <int MT, int G, int S>
+template <int RT, int G, int S>
 struct FewSmem {
-  static constexpr int kUnit = (MT * 4 + G * 4) * 512 + 256;   // weights, columns, scales (64 floats)
-  static constexpr int kRing = kFewWarps * S * kUnit;
-  static constexpr int kJoin = kFewWarps * MT * G * 512;
-  static constexpr int kBytes = kRing + kJoin;
-  static_assert(8 * G + 2 <= 64, "a unit's scales");
+  static constexpr int kKC = kFewWarps * kFewTiles / RT;
+  static constexpr int kChunkBytes = RT * 16 * 128;                      // a chunk's codes
+  // a column's records, an odd number of 64-byte halves apart: neighbouring columns use the other half of the banks
+  static constexpr int kColumn = (kKC * kFewRecord) % 128 == 64 ? kKC * kFewRecord : kKC * kFewRecord / 128 * 128 + 64 + (kKC * kFewRecord % 128 > 64 ? 128 : 0);
+  static constexpr int kScales = kKC * kChunkBytes + 8 * G * kColumn;    // 2 KC block scales
+  static constexpr int kStage = (kScales + 8 * kKC + 1023) / 1024 * 1024;
+  static constexpr int kRing = S * kStage;
+  static constexpr int kJoin = kFewWarps * kFewTiles * G * 512;
+  static constexpr int kBytes = 1024 + kRing + kJoin + 32 * S + 16;      // 1024: the ring's alignment
+  static_assert(kColumn >= kKC * kFewRecord && kColumn % 128 == 64, "column stride");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-template <int MODE, int MT, int G, int S>
-__global__ void __launch_bounds__(kFewThreads) few_weights_kernel(const FewArgs a) {
-  using Sm = FewSmem<MT, G, S>;
-  extern __shared__ __align__(128) uint8_t smem[];
+template <int MODE, int RT, int G, int S>
+__global__ void __launch_bounds__(kFewWeightThreads)
+few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_constant__ CUtensorMap map_hi,
+                   const FewArgs a) {
+  using Sm = FewSmem<RT, G, S>;
+  constexpr int KC = Sm::kKC;
+  constexpr int kRows = MODE == kFewGated ? 8 * RT : 16 * RT;            // output rows an item, and a box's
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* join = reinterpret_cast<float4*>(ring + Sm::kRing);
+  int4* stage_item = reinterpret_cast<int4*>(ring + Sm::kRing + Sm::kJoin);   // a stage's item: columns, first position, row
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_item + S);
+  uint64_t* empty = full + S;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + S);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 33);       // the bytes' announcement and the lanes that copy scales
+      mbar_init(&empty[s], kFewWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_launch();
+  pdl_wait();
   const int K = MODE == kFewDown ? a.I : a.H;
   const int N = MODE == kFewDown ? a.H : a.I;
-  constexpr int kRows = MODE == kFewGated ? 8 * MT : 16 * MT;      // output rows an item
   const int KB = K / 128;
-  const int row_blocks = N / kRows;
-  const int blocks = few_plan(a)->blocks;
-  const int64_t items = static_cast<int64_t>(blocks) * row_blocks;
-  const int* block_expert = few_at<const int>(a, a.l.block_expert);
-  const int* block_start = few_at<const int>(a, a.l.block_start);
-  const int* block_count = few_at<const int>(a, a.l.block_count);
+  const int steps = (KB + KC - 1) / KC;
+  const uint32_t blocks = few_plan(a)->blocks;
+  const uint32_t items = blocks * static_cast<uint32_t>(N / kRows);      // at most 1024 x 4096
   const int* entry = few_at<const int>(a, a.l.entry);
-  const uint8_t* w_lo = MODE == kFewDown ? a.wd : (MODE == kFewGated ? a.wg : a.wu);
-  const uint8_t* w_hi = MODE == kFewDown ? a.wd : a.wu;
-  const float* s_lo = MODE == kFewDown ? a.sd : (MODE == kFewGated ? a.sg : a.su);
-  const float* s_hi = MODE == kFewDown ? a.sd : a.su;
-  const __half* cols = few_at<const __half>(a, MODE == kFewDown ? a.l.hh : a.l.xh);
-  const float* col_scale = few_at<const float>(a, MODE == kFewDown ? a.l.hs : a.l.xs);
-  const int64_t ld_cs = MODE == kFewDown ? a.l.max_positions : a.l.ld_xs;
 
-  uint8_t* ring = smem + warp * S * Sm::kUnit;
-  const uint32_t ring_u32 = smem_u32(ring);
-  float4* join = reinterpret_cast<float4*>(smem + Sm::kRing);
-
-  // ---- the load cursor: (item, chunk) of the next unit to request ----
-  int64_t l_item = blockIdx.x;
-  int l_chunk = warp;
-  int l_slot = 0;
-  const uint8_t *p_lo[MT], *p_hi[MT];
-  const __half* p_col[G];
-  bool live[G];
-  const float *p_s0 = nullptr, *p_s1 = nullptr;   // this lane's one or two scales of the unit
-  int64_t ld_s0 = 0, ld_s1 = 0;
-  auto load_item = [&]() {
-    const int b = static_cast<int>(l_item % blocks);
-    const int row0 = static_cast<int>(l_item / blocks) * kRows;
-    const int64_t e = block_expert[b];
-    const int start = block_start[b], count = block_count[b];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r_lo = row0 + (MODE == kFewGated ? 8 * m : 16 * m) + g;
-      const int r_hi = MODE == kFewGated ? r_lo : r_lo + 8;
-      p_lo[m] = w_lo + (e * N + r_lo) * K + 16 * t;
-      p_hi[m] = w_hi + (e * N + r_hi) * K + 16 * t;
-    }
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int c = 8 * j + g;
-      live[j] = c < count;
-      const int64_t row = !live[j] ? 0 : (MODE == kFewDown ? start + c : entry[start + c] / a.k);
-      p_col[j] = cols + row * K + 16 * t;
-    }
-    // scales of a unit: [0, 8 G) the columns', 8 G and 8 G + 1 the weight rows'
-    const int64_t blk = (e * (N / 128) + row0 / 128) * KB;
-    auto scale_at = [&](int i, const float*& p, int64_t& ld) {
-      if (i < 8 * G) {
-        p = i < count ? col_scale + (MODE == kFewDown ? start + i : entry[start + i] / a.k) : nullptr;
-        ld = ld_cs;
-      } else {
-        p = i == 8 * G ? s_lo + blk : (i == 8 * G + 1 ? s_hi + blk : nullptr);
-        ld = 1;
-      }
+  if (warp >= kFewWarps) {
+    // ---- the loading warps: 0 the first half of a stage's boxes, 1 the other, the columns and the scales ----
+    const int half = warp - kFewWarps;
+    const int* block_expert = few_at<const int>(a, a.l.block_expert);
+    const int* block_start = few_at<const int>(a, a.l.block_start);
+    const int* block_count = few_at<const int>(a, a.l.block_count);
+    const uint8_t* records = few_at<const uint8_t>(a, MODE == kFewDown ? a.l.hr : a.l.xr);
+    // lanes 0 .. KC - 1 fetch the lower rows' scales, with a gate the next KC the upper rows'
+    const float* scales = MODE == kFewDown ? a.sd : (MODE == kFewGated ? (lane < KC ? a.sg : a.su) : a.su);
+    const int sc = lane % KC;
+    const CUtensorMap* map = MODE == kFewGated && half ? &map_hi : &map_lo;
+    struct Item {
+      int expert, start, count, row, record;      // record: this lane's column (or -1)
     };
-    scale_at(lane, p_s0, ld_s0);
-    scale_at(lane + 32, p_s1, ld_s1);
-  };
-  auto request = [&]() {
-    if (l_item < items && l_chunk < KB) {
-      const uint32_t unit = ring_u32 + l_slot * Sm::kUnit + lane * 16;
-      const int64_t o = static_cast<int64_t>(l_chunk) * 128;
+    auto look_up = [&](uint32_t item) {
+      Item i{0, 0, 0, 0, -1};
+      if (item < items) {
+        const uint32_t rb = item / blocks, b = item - rb * blocks;
+        i.expert = __ldg(block_expert + b);
+        i.start = __ldg(block_start + b);
+        i.count = __ldg(block_count + b);
+        i.row = static_cast<int>(rb) * kRows;
+      }
+      return i;
+    };
+    auto look_up_column = [&](Item& i) {
+      if (half && lane < i.count) i.record = MODE == kFewDown ? i.start + lane : __ldg(entry + i.start + lane) / a.k;
+    };
+    Item now = look_up(blockIdx.x);
+    look_up_column(now);
+    Item next = look_up(blockIdx.x + gridDim.x);
+    uint32_t it = 0, slot = 0, phase = 1;
+    bool ok = true;
+    for (uint32_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      look_up_column(next);
+      const Item after = look_up(item + 2 * gridDim.x);
+      const int row0 = now.expert * N + now.row;
+      const float* scale = scales + static_cast<int64_t>(row0 / 128) * KB + sc;
+      const uint8_t* col = records + static_cast<int64_t>(max(now.record, 0)) * KB * kFewRecord;
+      for (int c0 = 0; c0 < KB; c0 += KC) {
+        if (!warp_wait(&empty[slot], phase, abort_flag, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
+        const int n = min(KC, KB - c0);
+        uint8_t* stage = ring + slot * Sm::kStage;
+        if (lane == 0) {
+          if (!half) {
+            stage_item[slot] = make_int4(now.count, now.start, now.row, 0);
+            mbar_arrive_expect_tx(&full[slot], n * (Sm::kChunkBytes + now.count * kFewRecord));
+          }
+          if (MODE == kFewGated) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        cp_async16_or_zero(unit + (4 * m + 0) * 512, p_lo[m] + o, true);
-        cp_async16_or_zero(unit + (4 * m + 1) * 512, p_hi[m] + o, true);
-        cp_async16_or_zero(unit + (4 * m + 2) * 512, p_lo[m] + o + 64, true);
-        cp_async16_or_zero(unit + (4 * m + 3) * 512, p_hi[m] + o + 64, true);
-      }
+            for (int c = 0; c < KC; ++c)
+              if (c < n)
+                tma_load_2d_nohint(stage + c * Sm::kChunkBytes + half * RT * 1024, map, &full[slot], (c0 + c) * 128, row0);
+          } else {
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const uint32_t c = unit + (4 * MT + 4 * j) * 512;
-        cp_async16_or_zero(c, p_col[j] + o, live[j]);
-        cp_async16_or_zero(c + 512, p_col[j] + o + 8, live[j]);
-        cp_async16_or_zero(c + 1024, p_col[j] + o + 64, live[j]);
-        cp_async16_or_zero(c + 1536, p_col[j] + o + 72, live[j]);
+            for (int c = 0; c < KC / 2; ++c)
+              if (2 * c + half < n)
+                tma_load_2d_nohint(stage + (2 * c + half) * Sm::kChunkBytes, map, &full[slot], (c0 + 2 * c + half) * 128,
+                                   row0);
+          }
+        }
+        __syncwarp();
+        if (half) {
+          if (now.record >= 0)
+            bulk_load(stage + KC * Sm::kChunkBytes + lane * Sm::kColumn, col + c0 * kFewRecord, n * kFewRecord,
+                      &full[slot]);
+          if (lane < (MODE == kFewGated ? 2 * KC : KC) && sc < n)
+            cp_async4(stage + Sm::kScales + 4 * lane, scale + c0);
+          cp_async_arrive(&full[slot]);
+        }
+        ++it;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        phase ^= slot == 0 ? 1 : 0;
       }
-      const uint32_t sc = ring_u32 + l_slot * Sm::kUnit + (MT * 4 + G * 4) * 512 + lane * 4;
-      const float* any = s_lo;
-      cp_async4_or_zero(sc, p_s0 != nullptr ? p_s0 + l_chunk * ld_s0 : any, p_s0 != nullptr);
-      if (8 * G + 2 > 32) cp_async4_or_zero(sc + 128, p_s1 != nullptr ? p_s1 + l_chunk * ld_s1 : any, p_s1 != nullptr);
-      l_slot = l_slot + 1 == S ? 0 : l_slot + 1;
-      l_chunk += kFewWarps;
-      if (l_chunk >= KB) {
-        l_chunk = warp;
-        l_item += gridDim.x;
-        if (l_item < items) load_item();
-      }
+      now = next;
+      next = after;
     }
-    cp_async_commit();
-  };
-  if (l_item < items && warp < KB) load_item();
-  else l_item = items;                       // a warp without chunks requests nothing
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) request();
+    // a wait that gave up leaves copies in flight, which still write this block's memory
+    for (uint32_t j = it > S ? it - S : 0; j < it; ++j)
+      mbar_wait(&full[j % S], (j / S) & 1, nullptr, WAIT_DRAIN, 1ll << 22);
+    return;
+  }
 
-  int slot = 0;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    float acc[MT][G][4];
+  // ---- the multiplying warps ----
+  constexpr int TW = kFewTiles;
+  const int g = lane >> 2, t = lane & 3;
+  const int kc = warp % KC, rt0 = warp / KC * TW;
+  // codes: rows g of the two halves of the first tile; the next tile lies kTileStep further on
+  constexpr int kTileStep = (MODE == kFewGated ? 8 : 16) * 128;
+  const int code_lo = kc * Sm::kChunkBytes + (MODE == kFewGated ? 8 * rt0 + g : 16 * rt0 + g) * 128;
+  const int code_hi = code_lo + (MODE == kFewGated ? 8 * RT : 8) * 128;
+  const int sw0 = ((2 * t) ^ g) * 16, sw1 = ((2 * t + 1) ^ g) * 16;
+  const int col_at = KC * Sm::kChunkBytes + kc * kFewRecord;
+  uint32_t slot = 0, phase = 0;
+  bool ok = true;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    float acc[TW][G][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < TW; ++m)
 #pragma unroll
       for (int j = 0; j < G; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
-    const int b = static_cast<int>(item % blocks);
-    const int count = block_count[b], start = block_start[b];
-    const int row0 = static_cast<int>(item / blocks) * kRows;
-    for (int kb = warp; kb < KB; kb += kFewWarps) {
-      cp_async_wait<S - 2>();
-      __syncwarp();                          // the unit's scales; and the slot before it is free
-      request();
-      const uint8_t* unit = ring + slot * Sm::kUnit;
-      const uint4* u4 = reinterpret_cast<const uint4*>(unit) + lane;
-      const float* sc = reinterpret_cast<const float*>(unit + (MT * 4 + G * 4) * 512);
-      slot = slot + 1 == S ? 0 : slot + 1;
-      float part[MT][G][4];
+    int count = 0, start = 0, row0 = 0;
+    for (int st = 0; st < steps; ++st) {
+      const int kb = st * KC + kc;
+      if (ok) ok = warp_wait(&full[slot], phase, abort_flag, WAIT_MMA_FULL);
+      if (ok && st == 0) {
+        const int4 i = stage_item[slot];
+        count = i.x;
+        start = i.y;
+        row0 = i.z;
+      }
+      if (ok && kb < KB) {
+        const uint8_t* stage = ring + slot * Sm::kStage;
+        const float* block_scale = reinterpret_cast<const float*>(stage + Sm::kScales) + kc;
+        const float w0 = block_scale[0], w1 = MODE == kFewGated ? block_scale[KC] : w0;
+        float part[TW][G][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < TW; ++m)
 #pragma unroll
-        for (int j = 0; j < G; ++j)
+          for (int j = 0; j < G; ++j)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) part[m][j][c] = 0.0f;
+            for (int c = 0; c < 4; ++c) part[m][j][c] = 0.0f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t lo[MT][4], hi[MT][4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t l4[TW][4], h4[TW][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 p = u4[(4 * m + 2 * half) * 32], q = u4[(4 * m + 2 * half + 1) * 32];
-          lo[m][0] = p.x; lo[m][1] = p.y; lo[m][2] = p.z; lo[m][3] = p.w;
-          hi[m][0] = q.x; hi[m][1] = q.y; hi[m][2] = q.z; hi[m][3] = q.w;
-        }
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2) {     // eight of the piece's sixteen elements: two k16 steps
-          uint32_t al[MT][4], ah[MT][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            widen4(lo[m][2 * s2], al[m][0], al[m][1]);
-            widen4(lo[m][2 * s2 + 1], al[m][2], al[m][3]);
-            widen4(hi[m][2 * s2], ah[m][0], ah[m][1]);
-            widen4(hi[m][2 * s2 + 1], ah[m][2], ah[m][3]);
+          for (int m = 0; m < TW; ++m) {
+            const uint4 lo = *reinterpret_cast<const uint4*>(stage + code_lo + m * kTileStep + (h ? sw1 : sw0));
+            const uint4 hi = *reinterpret_cast<const uint4*>(stage + code_hi + m * kTileStep + (h ? sw1 : sw0));
+            l4[m][0] = lo.x; l4[m][1] = lo.y; l4[m][2] = lo.z; l4[m][3] = lo.w;
+            h4[m][0] = hi.x; h4[m][1] = hi.y; h4[m][2] = hi.z; h4[m][3] = hi.w;
           }
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            if (G > 1 && 8 * j >= count) continue;
-            const uint4 c = u4[(4 * MT + 4 * j + 2 * half + s2) * 32];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t al[TW][4], ah[TW][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma_f16(part[m][j], al[m][0], ah[m][0], al[m][1], ah[m][1], c.x, c.y);
-              mma_f16(part[m][j], al[m][2], ah[m][2], al[m][3], ah[m][3], c.z, c.w);
+            for (int m = 0; m < TW; ++m) {
+              widen4(l4[m][2 * q], al[m][0], al[m][1]);
+              widen4(l4[m][2 * q + 1], al[m][2], al[m][3]);
+              widen4(h4[m][2 * q], ah[m][0], ah[m][1]);
+              widen4(h4[m][2 * q + 1], ah[m][2], ah[m][3]);
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              if (G > 1 && 8 * j >= count) continue;
+              const uint4 c = *reinterpret_cast<const uint4*>(stage + col_at + (8 * j + g) * Sm::kColumn +
+                                                              (4 * (2 * h + q) + t) * 16);
+#pragma unroll
+              for (int m = 0; m < TW; ++m) mma_f16(part[m][j], al[m][0], ah[m][0], al[m][1], ah[m][1], c.x, c.y);
+#pragma unroll
+              for (int m = 0; m < TW; ++m) mma_f16(part[m][j], al[m][2], ah[m][2], al[m][3], ah[m][3], c.z, c.w);
             }
           }
         }
-      }
-      const float w0 = sc[8 * G], w1 = sc[8 * G + 1];
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const float2 cs = *reinterpret_cast<const float2*>(sc + 8 * j + 2 * t);
+        for (int j = 0; j < G; ++j) {
+          if (G > 1 && 8 * j >= count) continue;
+          const uint8_t* sc = stage + col_at + (8 * j + 2 * t) * Sm::kColumn + 256;
+          const float c0 = *reinterpret_cast<const float*>(sc), c1 = *reinterpret_cast<const float*>(sc + Sm::kColumn);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[m][j][0] = fmaf(part[m][j][0], w0 * cs.x, acc[m][j][0]);
-          acc[m][j][1] = fmaf(part[m][j][1], w0 * cs.y, acc[m][j][1]);
-          acc[m][j][2] = fmaf(part[m][j][2], w1 * cs.x, acc[m][j][2]);
-          acc[m][j][3] = fmaf(part[m][j][3], w1 * cs.y, acc[m][j][3]);
+          for (int m = 0; m < TW; ++m) {
+            acc[m][j][0] = fmaf(part[m][j][0], w0 * c0, acc[m][j][0]);
+            acc[m][j][1] = fmaf(part[m][j][1], w0 * c1, acc[m][j][1]);
+            acc[m][j][2] = fmaf(part[m][j][2], w1 * c0, acc[m][j][2]);
+            acc[m][j][3] = fmaf(part[m][j][3], w1 * c1, acc[m][j][3]);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      phase ^= slot == 0 ? 1 : 0;
     }
-    // join the warps' sums
+    few_join_barrier();                       // the item before has been read out of join
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < TW; ++m)
 #pragma unroll
       for (int j = 0; j < G; ++j)
-        join[(warp * MT * G + m * G + j) * 32 + lane] =
+        join[((kc * RT + rt0 + m) * G + j) * 32 + lane] =
             make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < MT * G * 32; i += kFewThreads) {
-      const int m = i / (G * 32), j = i / 32 % G;
-      if (8 * j >= count) continue;
+    few_join_barrier();
+    const int i = threadIdx.x;                // RT G 32 sums: one a thread
+    static_assert(RT * G <= kFewWarps, "one sum a thread");
+    const int m = i / (G * 32), j = i / 32 % G;
+    if (i < RT * G * 32 && 8 * j < count) {
       float4 s = join[i];
 #pragma unroll
-      for (int w = 1; w < kFewWarps; ++w) {
-        const float4 v = join[w * MT * G * 32 + i];
+      for (int u = 1; u < KC; ++u) {
+        const float4 v = join[u * RT * G * 32 + i];
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
-      // s: rows g and g + 8 (.xy, .zw) of tile m, columns 2 t and 2 t + 1 of group j
+      // rows g and g + 8 (.xy, .zw) of tile m, columns 2 t and 2 t + 1 of group j
       const float lo[2] = {s.x, s.y}, hi[2] = {s.z, s.w};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -472,23 +529,25 @@ __global__ void __launch_bounds__(kFewThreads) few_weights_kernel(const FewArgs 
         }
       }
     }
-    __syncthreads();                         // join is free for the next item
   }
 }
 
-// Hidden rows to FP16 chunks: a warp a chunk.
+// Hidden rows to FP16 records: a warp a chunk.
 __global__ void __launch_bounds__(kFewThreads) few_hidden_kernel(const FewArgs a) {
+  pdl_launch();
+  pdl_wait();
+  constexpr int kWarps = kFewThreads / 32;
   const int lane = threadIdx.x & 31;
   const int chunks = a.I / 128;
   const int items = few_plan(a)->positions * chunks;
   const int* entry = few_at<const int>(a, a.l.entry);
-  for (int item = blockIdx.x * kFewWarps + (threadIdx.x >> 5); item < items; item += gridDim.x * kFewWarps) {
-    const int p = item / chunks, kb = item - p * chunks;
+  for (int item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < items; item += gridDim.x * kWarps) {
+    const int p = item / chunks;
     if (entry[p] < 0) continue;
-    const int64_t o = static_cast<int64_t>(p) * a.I + kb * 128;
-    const float4 v = *reinterpret_cast<const float4*>(few_at<const float>(a, a.l.hid) + o + 4 * lane);
+    const float4 v = *reinterpret_cast<const float4*>(few_at<const float>(a, a.l.hid) + static_cast<int64_t>(item) * 128 +
+                                                      4 * lane);
     const float f[4] = {v.x, v.y, v.z, v.w};
-    few_chunk(f, few_at<__half>(a, a.l.hh) + o, few_at<float>(a, a.l.hs) + kb * a.l.max_positions + p, lane);
+    few_record(f, few_at<uint8_t>(a, a.l.hr) + static_cast<int64_t>(item) * kFewRecord, lane);
   }
 }
 
@@ -496,10 +555,12 @@ __global__ void __launch_bounds__(kFewThreads) few_hidden_kernel(const FewArgs a
 // whose slots names an expert gets zeros.  Eight columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(128) few_combine_kernel(const FewArgs a) {
+  pdl_wait();
   const int t = blockIdx.y;
   const int n = (blockIdx.x * 128 + threadIdx.x) * 8;
   if (n >= a.H) return;
   float s[8] = {};
+#pragma unroll 4
   for (int j = 0; j < a.k; ++j) {
     const int e = __ldg(a.ids + t * a.k + j);
     if (e < 0 || e >= a.E) continue;
