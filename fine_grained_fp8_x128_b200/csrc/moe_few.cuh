@@ -16,7 +16,7 @@
 //
 // Five launches, each started while the one before runs out (programmatic
 // dependent launch) and waiting for its end before any access:
-//   plan     tokens by expert in blocks of 8 G columns; x to FP16 records
+//   plan     tokens by expert in blocks of 8 columns; x to FP16 records
 //   up       hidden rows, FP32
 //   hidden   hidden rows to FP16 records
 //   down     each (token, slot)'s output row, FP32
@@ -36,7 +36,8 @@ constexpr int kFewMaxEntries = 1024;
 constexpr int kFewMaxExperts = 1024;
 constexpr int kFewThreads = 256;              // hidden
 constexpr int kFewWarps = 8;                  // of a weight pass, which multiply
-constexpr int kFewWeightThreads = 32 * (kFewWarps + 2);   // and two that load
+constexpr int kFewLoaders = 4;                // and of those that load
+constexpr int kFewWeightThreads = 32 * (kFewWarps + kFewLoaders);
 constexpr int kFewTiles = 2;                  // row tiles a multiplying warp takes
 constexpr int kFewRecord = 272;               // a chunk's 128 FP16 values and its scale, 16-byte units
 
@@ -157,7 +158,6 @@ __device__ __forceinline__ int2 few_scan(int2 v, int2 (&sums)[32]) {
 }
 
 // Block 0 orders the entries; the others turn x into FP16 chunks.
-template <int G>
 __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_launch();
@@ -189,15 +189,15 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
   }
   __syncthreads();
   const int c = count[tid];
-  const int2 mine = make_int2((c + 7) / 8 * 8, (c + 8 * G - 1) / (8 * G));   // padded positions, column blocks
+  const int2 mine = make_int2((c + 7) / 8 * 8, (c + 7) / 8);   // padded positions, column blocks
   const int2 upto = few_scan(mine, sums);
   start[tid] = upto.x - mine.x;
   for (int b = 0; b < mine.y; ++b) {
     const int at = upto.y - mine.y + b;
     if (chk(at, a.l.max_blocks, CHK_FEW)) {
       few_at<int>(a, a.l.block_expert)[at] = tid;
-      few_at<int>(a, a.l.block_start)[at] = upto.x - mine.x + 8 * G * b;
-      few_at<int>(a, a.l.block_count)[at] = min(c - 8 * G * b, 8 * G);
+      few_at<int>(a, a.l.block_start)[at] = upto.x - mine.x + 8 * b;
+      few_at<int>(a, a.l.block_count)[at] = min(c - 8 * b, 8);
     }
   }
   if (tid == 1023) {
@@ -217,19 +217,19 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
 
 // ---------------------------------------------------------------------------
 // The two weight passes.  An item is RT tiles of 16 weight rows of one expert
-// times one block of up to 8 G of its columns.  A block's 8 multiplying warps
+// times one block of up to 8 of its columns.  A block's 8 multiplying warps
 // take an item in stages of KC 128-wide K chunks, RT KC = 16: a warp multiplies two
 // tiles by one chunk of the stage, so that the columns' operands and a stage's
 // bookkeeping serve 4 KB of codes, and the warps' FP32 sums are joined once an
 // item, in chunk order.  (Sixteen warps of one tile each were bound by their
 // instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, where
 // the loads alone take 43.)
-// Two more warps keep the ring of S stages full, across items: TMA boxes of
-// rows x 128 bytes for the codes (half of the boxes each: one lane issues a
-// box in some 75 clocks), one bulk copy a column for its KC records, and the
-// stage's block scales, which start on no 16-byte boundary and so are per-thread
-// copies that arrive on the stage's barrier.  They look up an item's block and
-// columns while they load the item before, and hand it on with the stage.
+// Four more warps keep the ring of S stages full, across items.  One lane issues
+// a copy in some 100 clocks, so the work is spread: three warps issue the TMA
+// boxes of rows x 128 bytes, the fourth one bulk copy a column for its KC records
+// and the stage's block scales, which start on no 16-byte boundary and so are
+// per-thread copies that arrive on the stage's barrier.  They look up an item's
+// block and columns while they load the item before, and hand it on with the stage.
 //
 // Along K an instruction's operands may be taken in any order that both share:
 // lane (g, t) takes bytes 32 t .. 32 t + 31 of rows g and g + 8, which under the
@@ -265,26 +265,26 @@ __device__ __forceinline__ void few_join_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
 }
 
-template <int RT, int G, int S>
+template <int RT, int S>
 struct FewSmem {
   static constexpr int kKC = kFewWarps * kFewTiles / RT;
   static constexpr int kChunkBytes = RT * 16 * 128;                      // a chunk's codes
   // a column's records, an odd number of 64-byte halves apart: neighbouring columns use the other half of the banks
   static constexpr int kColumn = (kKC * kFewRecord) % 128 == 64 ? kKC * kFewRecord : kKC * kFewRecord / 128 * 128 + 64 + (kKC * kFewRecord % 128 > 64 ? 128 : 0);
-  static constexpr int kScales = kKC * kChunkBytes + 8 * G * kColumn;    // 2 KC block scales
+  static constexpr int kScales = kKC * kChunkBytes + 8 * kColumn;    // 2 KC block scales
   static constexpr int kStage = (kScales + 8 * kKC + 1023) / 1024 * 1024;
   static constexpr int kRing = S * kStage;
-  static constexpr int kJoin = kFewWarps * kFewTiles * G * 512;
+  static constexpr int kJoin = kFewWarps * kFewTiles * 512;
   static constexpr int kBytes = 1024 + kRing + kJoin + 32 * S + 16;      // 1024: the ring's alignment
   static_assert(kColumn >= kKC * kFewRecord && kColumn % 128 == 64, "column stride");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-template <int MODE, int RT, int G, int S>
+template <int MODE, int RT, int S>
 __global__ void __launch_bounds__(kFewWeightThreads)
 few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_constant__ CUtensorMap map_hi,
                    const FewArgs a) {
-  using Sm = FewSmem<RT, G, S>;
+  using Sm = FewSmem<RT, S>;
   constexpr int KC = Sm::kKC;
   constexpr int kRows = MODE == kFewGated ? 8 * RT : 16 * RT;            // output rows an item, and a box's
   extern __shared__ uint8_t smem_raw[];
@@ -316,8 +316,10 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   const int* entry = few_at<const int>(a, a.l.entry);
 
   if (warp >= kFewWarps) {
-    // ---- the loading warps: 0 the first half of a stage's boxes, 1 the other, the columns and the scales ----
-    const int half = warp - kFewWarps;
+    // ---- the loading warps: the last one the columns and the scales, the others the boxes in turn ----
+    const int loader = warp - kFewWarps;
+    constexpr int kBoxLoaders = kFewLoaders - 1, kBoxes = MODE == kFewGated ? 2 * KC : KC;
+    const bool columns = loader == kBoxLoaders;
     const int* block_expert = few_at<const int>(a, a.l.block_expert);
     const int* block_start = few_at<const int>(a, a.l.block_start);
     const int* block_count = few_at<const int>(a, a.l.block_count);
@@ -325,7 +327,6 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
     // lanes 0 .. KC - 1 fetch the lower rows' scales, with a gate the next KC the upper rows'
     const float* scales = MODE == kFewDown ? a.sd : (MODE == kFewGated ? (lane < KC ? a.sg : a.su) : a.su);
     const int sc = lane % KC;
-    const CUtensorMap* map = MODE == kFewGated && half ? &map_hi : &map_lo;
     struct Item {
       int expert, start, count, row, record;      // record: this lane's column (or -1)
     };
@@ -341,7 +342,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
       return i;
     };
     auto look_up_column = [&](Item& i) {
-      if (half && lane < i.count) i.record = MODE == kFewDown ? i.start + lane : __ldg(entry + i.start + lane) / a.k;
+      if (columns && lane < i.count) i.record = MODE == kFewDown ? i.start + lane : __ldg(entry + i.start + lane) / a.k;
     };
     Item now = look_up(blockIdx.x);
     look_up_column(now);
@@ -358,33 +359,26 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
         if (!warp_wait(&empty[slot], phase, abort_flag, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
         const int n = min(KC, KB - c0);
         uint8_t* stage = ring + slot * Sm::kStage;
-        if (lane == 0) {
-          if (!half) {
-            stage_item[slot] = make_int4(now.count, now.start, now.row, 0);
-            mbar_arrive_expect_tx(&full[slot], n * (Sm::kChunkBytes + now.count * kFewRecord));
-          }
-          if (MODE == kFewGated) {
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-              if (c < n)
-                tma_load_2d_nohint(stage + c * Sm::kChunkBytes + half * RT * 1024, map, &full[slot], (c0 + c) * 128, row0);
-          } else {
-#pragma unroll
-            for (int c = 0; c < KC / 2; ++c)
-              if (2 * c + half < n)
-                tma_load_2d_nohint(stage + (2 * c + half) * Sm::kChunkBytes, map, &full[slot], (c0 + 2 * c + half) * 128,
-                                   row0);
-          }
-        }
-        __syncwarp();
-        if (half) {
+        if (columns) {
           if (now.record >= 0)
             bulk_load(stage + KC * Sm::kChunkBytes + lane * Sm::kColumn, col + c0 * kFewRecord, n * kFewRecord,
                       &full[slot]);
-          if (lane < (MODE == kFewGated ? 2 * KC : KC) && sc < n)
-            cp_async4(stage + Sm::kScales + 4 * lane, scale + c0);
+          if (lane < kBoxes && sc < n) cp_async4(stage + Sm::kScales + 4 * lane, scale + c0);
           cp_async_arrive(&full[slot]);
+        } else if (lane == 0) {
+          if (loader == 0) {
+            stage_item[slot] = make_int4(now.count, now.start, now.row, 0);
+            mbar_arrive_expect_tx(&full[slot], n * (Sm::kChunkBytes + now.count * kFewRecord));
+          }
+#pragma unroll
+          for (int i = 0; i < (kBoxes + kBoxLoaders - 1) / kBoxLoaders; ++i) {
+            const int box = i * kBoxLoaders + loader, c = box % KC;      // with a gate: KC boxes of it, then of the other
+            if (box < kBoxes && c < n)
+              tma_load_2d_nohint(stage + c * Sm::kChunkBytes + (box >= KC ? RT * 1024 : 0), box >= KC ? &map_hi : &map_lo,
+                                 &full[slot], (c0 + c) * 128, row0);
+          }
         }
+        __syncwarp();
         ++it;
         slot = slot + 1 == S ? 0 : slot + 1;
         phase ^= slot == 0 ? 1 : 0;
@@ -411,13 +405,11 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   uint32_t slot = 0, phase = 0;
   bool ok = true;
   for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    float acc[TW][G][4];
+    float acc[TW][4];
 #pragma unroll
     for (int m = 0; m < TW; ++m)
 #pragma unroll
-      for (int j = 0; j < G; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
+      for (int c = 0; c < 4; ++c) acc[m][c] = 0.0f;
     int count = 0, start = 0, row0 = 0;
     for (int st = 0; st < steps; ++st) {
       const int kb = st * KC + kc;
@@ -432,13 +424,11 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
         const uint8_t* stage = ring + slot * Sm::kStage;
         const float* block_scale = reinterpret_cast<const float*>(stage + Sm::kScales) + kc;
         const float w0 = block_scale[0], w1 = MODE == kFewGated ? block_scale[KC] : w0;
-        float part[TW][G][4];
+        float part[TW][4];
 #pragma unroll
         for (int m = 0; m < TW; ++m)
 #pragma unroll
-          for (int j = 0; j < G; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) part[m][j][c] = 0.0f;
+          for (int c = 0; c < 4; ++c) part[m][c] = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t l4[TW][4], h4[TW][4];
@@ -459,30 +449,21 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
               widen4(h4[m][2 * q], ah[m][0], ah[m][1]);
               widen4(h4[m][2 * q + 1], ah[m][2], ah[m][3]);
             }
+            const uint4 c = *reinterpret_cast<const uint4*>(stage + col_at + g * Sm::kColumn + (4 * (2 * h + q) + t) * 16);
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-              if (G > 1 && 8 * j >= count) continue;
-              const uint4 c = *reinterpret_cast<const uint4*>(stage + col_at + (8 * j + g) * Sm::kColumn +
-                                                              (4 * (2 * h + q) + t) * 16);
+            for (int m = 0; m < TW; ++m) mma_f16(part[m], al[m][0], ah[m][0], al[m][1], ah[m][1], c.x, c.y);
 #pragma unroll
-              for (int m = 0; m < TW; ++m) mma_f16(part[m][j], al[m][0], ah[m][0], al[m][1], ah[m][1], c.x, c.y);
-#pragma unroll
-              for (int m = 0; m < TW; ++m) mma_f16(part[m][j], al[m][2], ah[m][2], al[m][3], ah[m][3], c.z, c.w);
-            }
+            for (int m = 0; m < TW; ++m) mma_f16(part[m], al[m][2], ah[m][2], al[m][3], ah[m][3], c.z, c.w);
           }
         }
+        const uint8_t* sc = stage + col_at + 2 * t * Sm::kColumn + 256;
+        const float c0 = *reinterpret_cast<const float*>(sc), c1 = *reinterpret_cast<const float*>(sc + Sm::kColumn);
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          if (G > 1 && 8 * j >= count) continue;
-          const uint8_t* sc = stage + col_at + (8 * j + 2 * t) * Sm::kColumn + 256;
-          const float c0 = *reinterpret_cast<const float*>(sc), c1 = *reinterpret_cast<const float*>(sc + Sm::kColumn);
-#pragma unroll
-          for (int m = 0; m < TW; ++m) {
-            acc[m][j][0] = fmaf(part[m][j][0], w0 * c0, acc[m][j][0]);
-            acc[m][j][1] = fmaf(part[m][j][1], w0 * c1, acc[m][j][1]);
-            acc[m][j][2] = fmaf(part[m][j][2], w1 * c0, acc[m][j][2]);
-            acc[m][j][3] = fmaf(part[m][j][3], w1 * c1, acc[m][j][3]);
-          }
+        for (int m = 0; m < TW; ++m) {
+          acc[m][0] = fmaf(part[m][0], w0 * c0, acc[m][0]);
+          acc[m][1] = fmaf(part[m][1], w0 * c1, acc[m][1]);
+          acc[m][2] = fmaf(part[m][2], w1 * c0, acc[m][2]);
+          acc[m][3] = fmaf(part[m][3], w1 * c1, acc[m][3]);
         }
       }
       __syncwarp();
@@ -493,26 +474,22 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
     few_join_barrier();                       // the item before has been read out of join
 #pragma unroll
     for (int m = 0; m < TW; ++m)
-#pragma unroll
-      for (int j = 0; j < G; ++j)
-        join[((kc * RT + rt0 + m) * G + j) * 32 + lane] =
-            make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+      join[(kc * RT + rt0 + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
     few_join_barrier();
-    const int i = threadIdx.x;                // RT G 32 sums: one a thread
-    static_assert(RT * G <= kFewWarps, "one sum a thread");
-    const int m = i / (G * 32), j = i / 32 % G;
-    if (i < RT * G * 32 && 8 * j < count) {
-      float4 s = join[i];
+    static_assert(RT <= kFewWarps, "a tile's sums a warp");
+    if (warp < RT) {
+      const int m = warp;
+      float4 s = join[m * 32 + lane];
 #pragma unroll
       for (int u = 1; u < KC; ++u) {
-        const float4 v = join[u * RT * G * 32 + i];
+        const float4 v = join[(u * RT + m) * 32 + lane];
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
-      // rows g and g + 8 (.xy, .zw) of tile m, columns 2 t and 2 t + 1 of group j
+      // rows g and g + 8 (.xy, .zw) of the tile, columns 2 t and 2 t + 1
       const float lo[2] = {s.x, s.y}, hi[2] = {s.z, s.w};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int col = 8 * j + 2 * t + c;
+        const int col = 2 * t + c;
         if (col >= count) continue;
         const int at = start + col;
         if (MODE == kFewGated) {
@@ -552,24 +529,26 @@ __global__ void __launch_bounds__(kFewThreads) few_hidden_kernel(const FewArgs a
 }
 
 // y[t] = sum_j share[t,j] * (slot j's row), in slot order; a token none of
-// whose slots names an expert gets zeros.  Eight columns a thread.
+// whose slots names an expert gets zeros.  Eight columns a thread; a skipped
+// slot's row is read with the others (its place holds anything) and not used.
 template <typename T>
-__global__ void __launch_bounds__(128) few_combine_kernel(const FewArgs a) {
-  pdl_wait();
+__global__ void __launch_bounds__(64) few_combine_kernel(const FewArgs a) {
   const int t = blockIdx.y;
-  const int n = (blockIdx.x * 128 + threadIdx.x) * 8;
+  const int n = (blockIdx.x * 64 + threadIdx.x) * 8;
+  pdl_wait();
   if (n >= a.H) return;
   float s[8] = {};
-#pragma unroll 4
+  const float* rows = few_at<const float>(a, a.l.yp) + static_cast<int64_t>(t) * a.k * a.H + n;
+#pragma unroll 8
   for (int j = 0; j < a.k; ++j) {
     const int e = __ldg(a.ids + t * a.k + j);
-    if (e < 0 || e >= a.E) continue;
     const float w = __ldg(a.share + t * a.k + j);
-    const float4* src = reinterpret_cast<const float4*>(few_at<const float>(a, a.l.yp) +
-                                                        (static_cast<int64_t>(t) * a.k + j) * a.H + n);
+    const float4* src = reinterpret_cast<const float4*>(rows + static_cast<int64_t>(j) * a.H);
     const float4 u = src[0], v = src[1];
-    s[0] = fmaf(w, u.x, s[0]); s[1] = fmaf(w, u.y, s[1]); s[2] = fmaf(w, u.z, s[2]); s[3] = fmaf(w, u.w, s[3]);
-    s[4] = fmaf(w, v.x, s[4]); s[5] = fmaf(w, v.y, s[5]); s[6] = fmaf(w, v.z, s[6]); s[7] = fmaf(w, v.w, s[7]);
+    if (e >= 0 && e < a.E) {
+      s[0] = fmaf(w, u.x, s[0]); s[1] = fmaf(w, u.y, s[1]); s[2] = fmaf(w, u.z, s[2]); s[3] = fmaf(w, u.w, s[3]);
+      s[4] = fmaf(w, v.x, s[4]); s[5] = fmaf(w, v.y, s[5]); s[6] = fmaf(w, v.z, s[6]); s[7] = fmaf(w, v.w, s[7]);
+    }
   }
   Raw8<T> o;
   pack8(o, s);
