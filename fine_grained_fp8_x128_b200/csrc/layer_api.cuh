@@ -100,11 +100,11 @@ fp8q_status launch_after(Kern kern, dim3 grid, int threads, int smem, cudaStream
   return FP8Q_OK;
 }
 
-template <int MODE, int RT, int TEAMS, int S>
+template <int MODE, int RT, int S>
 fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  using Sm = fp8q::FewSmem<RT, TEAMS, S>;
-  auto kern = fp8q::few_weights_kernel<MODE, RT, TEAMS, S>;
+  using Sm = fp8q::FewSmem<RT, S>;
+  auto kern = fp8q::few_weights_kernel<MODE, RT, S>;
   fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
   if (st != FP8Q_OK) return st;
   const int64_t K = MODE == fp8q::kFewDown ? a.I : a.H, rows = static_cast<int64_t>(a.E) * (MODE == fp8q::kFewDown ? a.H : a.I);
@@ -113,23 +113,23 @@ fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStre
   if ((st = make_tmap(&map_lo, lo, K, rows, K, MODE == fp8q::kFewGated ? 8 * RT : 16 * RT)) != FP8Q_OK) return st;
   map_hi = map_lo;
   if (MODE == fp8q::kFewGated && (st = make_tmap(&map_hi, a.wu, K, rows, K, 8 * RT)) != FP8Q_OK) return st;
-  return launch_after(kern, dim3(dev->sm_count), Sm::kThreads, Sm::kBytes, s, map_lo, map_hi, a);
+  return launch_after(kern, dim3(dev->sm_count), fp8q::kFewWeightThreads, Sm::kBytes, s, map_lo, map_hi, a);
 }
 
-template <int RT, int TEAMS, int S>
+template <int RT, int S>
 fp8q_status moe_few(const fp8q::FewArgs& a, int y_dtype, DeviceInfo* dev, cudaStream_t s) {
   fp8q_status st;
   fp8q::few_plan_kernel<<<static_cast<unsigned>(1 + ceil_div(static_cast<int64_t>(a.T) * (a.H / 128), 32)), 1024, 0,
                              s>>>(a);
   if ((st = launch_status()) != FP8Q_OK) return st;
-  st = a.wg != nullptr ? launch_few_weights<fp8q::kFewGated, RT, TEAMS, S>(a, dev, s)
-                       : launch_few_weights<fp8q::kFewPlain, RT, TEAMS, S>(a, dev, s);
+  st = a.wg != nullptr ? launch_few_weights<fp8q::kFewGated, RT, S>(a, dev, s)
+                       : launch_few_weights<fp8q::kFewPlain, RT, S>(a, dev, s);
   if (st != FP8Q_OK) return st;
   const int64_t chunks = a.l.max_positions * (a.I / 128);
   const int64_t grid = grid_for(ceil_div(chunks, fp8q::kFewThreads / 32), dev->sm_count, 8);
   st = launch_after(fp8q::few_hidden_kernel, dim3(static_cast<unsigned>(grid)), fp8q::kFewThreads, 0, s, a);
   if (st != FP8Q_OK) return st;
-  if ((st = launch_few_weights<fp8q::kFewDown, RT, TEAMS, S>(a, dev, s)) != FP8Q_OK) return st;
+  if ((st = launch_few_weights<fp8q::kFewDown, RT, S>(a, dev, s)) != FP8Q_OK) return st;
   const dim3 cg(static_cast<unsigned>(ceil_div(a.H, 512)), static_cast<unsigned>(a.T));
   return y_dtype == FP8Q_OUT_F32 ? launch_after(fp8q::few_combine_kernel<float>, cg, 64, 0, s, a)
                                  : launch_after(fp8q::few_combine_kernel<__nv_bfloat16>, cg, 64, 0, s, a);
@@ -335,12 +335,11 @@ fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx
   a.ws = static_cast<uint8_t*>(workspace);
   a.l = fp8q::few_layout(T, k, E, H, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Row tiles an item and teams: few entries need small items to fill the SMs evenly, many are better off with fewer,
-  // larger boxes and a second team.  7168 -> 2048 -> 7168, top-8, the whole call with 2 tiles and a team, 4 and a team,
-  // 8 and two teams (us): 1 token 69, 75, 76; 4 tokens 145, 147, 148; 16 tokens (64 experts, no gate) 215, 214, 221;
-  // 128 tokens (256 experts, calls in a row) 1820, 1755, 1610.
-  if (T * k <= 64) return moe_few<2, 1, 4>(a, y_dtype, dev, s);
-  return T * k <= 256 ? moe_few<4, 1, 5>(a, y_dtype, dev, s) : moe_few<8, 2, 4>(a, y_dtype, dev, s);
+  // Row tiles an item: few entries need small items to fill the SMs evenly, many are better off with fewer, larger
+  // boxes.  7168 -> 2048 -> 7168, top-8, the whole call with 2, 4 and 8 tiles (us): 1 token 69, 75, 75; 4 tokens 145,
+  // 147, 148; 16 tokens (64 experts, no gate) 215, 214, 220; 128 tokens 1480, 1405, 1367.
+  if (T * k <= 64) return moe_few<2, 4>(a, y_dtype, dev, s);
+  return T * k <= 512 ? moe_few<4, 5>(a, y_dtype, dev, s) : moe_few<8, 5>(a, y_dtype, dev, s);
 }
 
 int64_t fp8q_lora_apply_workspace(int64_t T, int64_t K, int64_t r, int64_t groups) {

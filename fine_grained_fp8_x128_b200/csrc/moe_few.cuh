@@ -35,8 +35,9 @@ constexpr int kFewMaxTokens = 128;
 constexpr int kFewMaxEntries = 1024;
 constexpr int kFewMaxExperts = 1024;
 constexpr int kFewThreads = 256;              // hidden
-constexpr int kFewTeam = 8;                   // warps that multiply a stage of a weight pass
-constexpr int kFewLoaders = 4;                // and warps that load
+constexpr int kFewWarps = 8;                  // of a weight pass, which multiply
+constexpr int kFewLoaders = 4;                // and of those that load
+constexpr int kFewWeightThreads = 32 * (kFewWarps + kFewLoaders);
 constexpr int kFewTiles = 2;                  // row tiles a multiplying warp takes
 constexpr int kFewRecord = 272;               // a chunk's 128 FP16 values and its scale, 16-byte units
 
@@ -216,18 +217,13 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
 
 // ---------------------------------------------------------------------------
 // The two weight passes.  An item is RT tiles of 16 weight rows of one expert
-// times one block of up to 8 of its columns, taken in stages of KC 128-wide K
-// chunks, RT KC = 16.  A team of 8 warps multiplies a stage, two tiles by one
-// chunk a warp, so that the columns' operands and a stage's bookkeeping serve 4 KB
-// of codes; the warps' FP32 sums are joined once an item, in a fixed order.
-// (Sixteen warps of one tile each were bound by their instructions.)
-// With many tokens a team is bound by its own latency (900 of a stage's 1100
-// clocks), and two teams take the stages in turn: 128 tokens of 256 experts
-// 1610 us instead of 1700 in a row of calls, under the power cap.  With one token
-// the loads are the bound and the second team only costs (73 us instead of 69).
-// A ring slot belongs to one team for good: a wait on a barrier's parity is only
-// sound for who has seen the phase before it, and so consumed the slot's last round.
-//
+// times one block of up to 8 of its columns.  A block's 8 multiplying warps
+// take an item in stages of KC 128-wide K chunks, RT KC = 16: a warp multiplies two
+// tiles by one chunk of the stage, so that the columns' operands and a stage's
+// bookkeeping serve 4 KB of codes, and the warps' FP32 sums are joined once an
+// item, in chunk order.  (Sixteen warps of one tile each were bound by their
+// instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, where
+// the loads alone take 43.)
 // Four more warps keep the ring of S stages full, across items.  One lane issues
 // a copy in some 100 clocks, so the work is spread: three warps issue the TMA
 // boxes of rows x 128 bytes, the fourth one bulk copy a column for its KC records
@@ -264,29 +260,31 @@ __device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The multiplying warps' own barrier.
+__device__ __forceinline__ void few_join_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+}
 
-template <int RT, int TEAMS, int S>
+template <int RT, int S>
 struct FewSmem {
-  static constexpr int kWarps = TEAMS * kFewTeam;
-  static constexpr int kThreads = 32 * (kWarps + kFewLoaders);
-  static constexpr int kKC = kFewTeam * kFewTiles / RT;
+  static constexpr int kKC = kFewWarps * kFewTiles / RT;
   static constexpr int kChunkBytes = RT * 16 * 128;                      // a chunk's codes
   // a column's records, an odd number of 64-byte halves apart: neighbouring columns use the other half of the banks
   static constexpr int kColumn = (kKC * kFewRecord) % 128 == 64 ? kKC * kFewRecord : kKC * kFewRecord / 128 * 128 + 64 + (kKC * kFewRecord % 128 > 64 ? 128 : 0);
   static constexpr int kScales = kKC * kChunkBytes + 8 * kColumn;    // 2 KC block scales
   static constexpr int kStage = (kScales + 8 * kKC + 1023) / 1024 * 1024;
   static constexpr int kRing = S * kStage;
-  static constexpr int kJoin = kWarps * kFewTiles * 512;
+  static constexpr int kJoin = kFewWarps * kFewTiles * 512;
   static constexpr int kBytes = 1024 + kRing + kJoin + 32 * S + 16;      // 1024: the ring's alignment
   static_assert(kColumn >= kKC * kFewRecord && kColumn % 128 == 64, "column stride");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-template <int MODE, int RT, int TEAMS, int S>
-__global__ void __launch_bounds__(FewSmem<RT, TEAMS, S>::kThreads)
+template <int MODE, int RT, int S>
+__global__ void __launch_bounds__(kFewWeightThreads)
 few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_constant__ CUtensorMap map_hi,
                    const FewArgs a) {
-  using Sm = FewSmem<RT, TEAMS, S>;
+  using Sm = FewSmem<RT, S>;
   constexpr int KC = Sm::kKC;
   constexpr int kRows = MODE == kFewGated ? 8 * RT : 16 * RT;            // output rows an item, and a box's
   extern __shared__ uint8_t smem_raw[];
@@ -301,7 +299,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 33);       // the bytes' announcement and the lanes that copy scales
-      mbar_init(&empty[s], kFewTeam);
+      mbar_init(&empty[s], kFewWarps);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -317,9 +315,9 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   const uint32_t items = blocks * static_cast<uint32_t>(N / kRows);      // at most 1024 x 4096
   const int* entry = few_at<const int>(a, a.l.entry);
 
-  if (warp >= Sm::kWarps) {
+  if (warp >= kFewWarps) {
     // ---- the loading warps: the last one the columns and the scales, the others the boxes in turn ----
-    const int loader = warp - Sm::kWarps;
+    const int loader = warp - kFewWarps;
     constexpr int kBoxLoaders = kFewLoaders - 1, kBoxes = MODE == kFewGated ? 2 * KC : KC;
     const bool columns = loader == kBoxLoaders;
     const int* block_expert = few_at<const int>(a, a.l.block_expert);
@@ -397,18 +395,14 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   // ---- the multiplying warps ----
   constexpr int TW = kFewTiles;
   const int g = lane >> 2, t = lane & 3;
-  const int team = warp / kFewTeam, kc = warp % KC, rt0 = warp % kFewTeam / KC * TW;
+  const int kc = warp % KC, rt0 = warp / KC * TW;
   // codes: rows g of the two halves of the first tile; the next tile lies kTileStep further on
   constexpr int kTileStep = (MODE == kFewGated ? 8 : 16) * 128;
   const int code_lo = kc * Sm::kChunkBytes + (MODE == kFewGated ? 8 * rt0 + g : 16 * rt0 + g) * 128;
   const int code_hi = code_lo + (MODE == kFewGated ? 8 * RT : 8) * 128;
   const int sw0 = ((2 * t) ^ g) * 16, sw1 = ((2 * t + 1) ^ g) * 16;
   const int col_at = KC * Sm::kChunkBytes + kc * kFewRecord;
-  uint32_t slot = 0, phase = 0;              // of the next stage, whoever's it is
-  auto advance = [&]() {
-    slot = slot + 1 == S ? 0 : slot + 1;
-    phase ^= slot == 0 ? 1 : 0;
-  };
+  uint32_t slot = 0, phase = 0;
   bool ok = true;
   for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
     float acc[TW][4];
@@ -417,10 +411,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][c] = 0.0f;
     int count = 0, start = 0, row0 = 0;
-    static_assert(S % TEAMS == 0, "a slot belongs to one team");
-    const bool first = static_cast<int>(slot % TEAMS) == team;     // whether this team takes the item's first stage
-    for (int st = 0; st < steps; ++st, advance()) {
-      if (static_cast<int>(slot % TEAMS) != team) continue;
+    for (int st = 0; st < steps; ++st) {
       const int kb = st * KC + kc;
       if (ok) ok = warp_wait(&full[slot], phase, abort_flag, WAIT_MMA_FULL);
       if (ok && st == 0) {
@@ -477,20 +468,20 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      phase ^= slot == 0 ? 1 : 0;
     }
-    // the multiplying warps' own barrier
-    auto join_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * Sm::kWarps) : "memory"); };
-    join_barrier();                           // the item before has been read out of join
+    few_join_barrier();                       // the item before has been read out of join
 #pragma unroll
     for (int m = 0; m < TW; ++m)
-      join[(((first ? 0 : KC) + kc) * RT + rt0 + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
-    join_barrier();
-    static_assert(RT <= kFewTeam, "a tile's sums a warp");
-    const int m = warp % kFewTeam;
-    if (first && m < RT) {                     // the team that knows the item adds up, a tile a warp
+      join[(kc * RT + rt0 + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+    few_join_barrier();
+    static_assert(RT <= kFewWarps, "a tile's sums a warp");
+    if (warp < RT) {
+      const int m = warp;
       float4 s = join[m * 32 + lane];
 #pragma unroll
-      for (int u = 1; u < TEAMS * KC; ++u) {
+      for (int u = 1; u < KC; ++u) {
         const float4 v = join[(u * RT + m) * 32 + lane];
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
