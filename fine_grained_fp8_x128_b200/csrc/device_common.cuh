@@ -32,6 +32,7 @@ enum : uint32_t {
   BAD_ROW_INDEX = 8,
   BAD_EXPERT_ID = 9,
   BAD_COUNT_TABLE = 10,
+  WAIT_STAGE = 11,
 };
 
 __device__ __forceinline__ void report_status(uint32_t code, uint32_t where) {

@@ -9,64 +9,6 @@ inline bool bad_dtype(int dt) { return dt != FP8Q_OUT_BF16 && dt != FP8Q_OUT_F32
 inline int64_t elem_size(int dt) { return dt == FP8Q_OUT_F32 ? 4 : 2; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a layer norm row of N elements is laid over threads: one warp up to 512
-// elements, else a block with one vector of eight elements a thread (two above
-// `one_vec` elements).
-struct NormShape {
-  bool warp_row;
-  int vpt;
-  int threads;
-};
-NormShape norm_shape(int64_t N, int64_t one_vec) {
-  NormShape s;
-  const int64_t vecs = ceil_div(N, 8);
-  s.warp_row = N <= fp8q::kNormWarpRowMaxN;
-  s.vpt = s.warp_row ? (N <= 256 ? 1 : 2) : (N <= one_vec ? 1 : 2);
-  s.threads = s.warp_row ? fp8q::kNormWarpRowThreads : static_cast<int>(ceil_div(ceil_div(vecs, s.vpt), 32) * 32);
-  return s;
-}
-constexpr int64_t kNormFwdOneVec = 4096;    // 512 threads
-constexpr int64_t kNormBwdOneVec = 8192;    // 1024 threads
-
-// Blocks of the backward pass, and so partial rows: a function of the sizes
-// alone, so that the same call always adds in the same order.
-int64_t norm_bwd_blocks(int64_t M, int64_t N) {
-  const NormShape s = norm_shape(N, kNormBwdOneVec);
-  const int64_t rows = s.warp_row ? 2 * (fp8q::kNormWarpRowThreads / 32) : 2;
-  const int64_t cap = 148 * (s.threads > 512 ? 1 : (s.threads > 256 ? 2 : 4));
-  const int64_t b = ceil_div(M, rows);
-  return b < cap ? b : cap;
-}
-
-template <typename T, typename W, int VPT, bool kWarpRow>
-void launch_norm(const fp8q::LayerNormArgs& a, int64_t grid, int threads, cudaStream_t s) {
-  if (a.q != nullptr)
-    fp8q::layer_norm_kernel<T, W, VPT, kWarpRow, true><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
-  else
-    fp8q::layer_norm_kernel<T, W, VPT, kWarpRow, false><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
-}
-template <typename T, typename W>
-void launch_norm_shape(const fp8q::LayerNormArgs& a, const NormShape& sh, int64_t grid, cudaStream_t s) {
-  if (sh.warp_row) {
-    if (sh.vpt == 1) launch_norm<T, W, 1, true>(a, grid, sh.threads, s);
-    else launch_norm<T, W, 2, true>(a, grid, sh.threads, s);
-  } else {
-    if (sh.vpt == 1) launch_norm<T, W, 1, false>(a, grid, sh.threads, s);
-    else launch_norm<T, W, 2, false>(a, grid, sh.threads, s);
-  }
-}
-template <typename T, typename W>
-void launch_norm_bwd(const fp8q::LayerNormBwdArgs& a, const NormShape& sh, int64_t grid, cudaStream_t s) {
-  const unsigned g = static_cast<unsigned>(grid);
-  if (sh.warp_row) {
-    if (sh.vpt == 1) fp8q::layer_norm_bwd_kernel<T, W, 1, true><<<g, sh.threads, 0, s>>>(a);
-    else fp8q::layer_norm_bwd_kernel<T, W, 2, true><<<g, sh.threads, 0, s>>>(a);
-  } else {
-    if (sh.vpt == 1) fp8q::layer_norm_bwd_kernel<T, W, 1, false><<<g, sh.threads, 0, s>>>(a);
-    else fp8q::layer_norm_bwd_kernel<T, W, 2, false><<<g, sh.threads, 0, s>>>(a);
-  }
-}
-
 // Dynamic shared memory of a kernel instance, set once per device.
 template <class Kern>
 fp8q_status allow_smem(Kern kern, int bytes, bool* done) {
@@ -98,6 +40,110 @@ fp8q_status launch_after(Kern kern, dim3 grid, int threads, int smem, cudaStream
     return FP8Q_ERR_CUDA;
   }
   return FP8Q_OK;
+}
+
+// How a layer norm row of N elements is laid over threads: one warp up to 512
+// elements, else a block with one vector of eight elements a thread (two above
+// `one_vec` elements).
+struct NormShape {
+  bool warp_row;
+  int vpt;
+  int threads;
+};
+NormShape norm_shape(int64_t N, int64_t one_vec) {
+  NormShape s;
+  const int64_t vecs = ceil_div(N, 8);
+  s.warp_row = N <= fp8q::kNormWarpRowMaxN;
+  s.vpt = s.warp_row ? (N <= 256 ? 1 : 2) : (N <= one_vec ? 1 : 2);
+  s.threads = s.warp_row ? fp8q::kNormWarpRowThreads : static_cast<int>(ceil_div(ceil_div(vecs, s.vpt), 32) * 32);
+  return s;
+}
+constexpr int64_t kNormFwdOneVec = 4096;    // 512 threads
+constexpr int64_t kNormBwdOneVec = 8192;    // 1024 threads
+
+// Many rows of whole vectors go through the stream kernels: from four steps an
+// SM on, where the ring's start no longer shows, and while a stage of `rows`
+// rows of `bytes` a column fits a third of an SM's shared memory.
+bool norm_streams(int64_t M, int64_t N, int rows, int64_t bytes) {
+  return N % 8 == 0 && N > fp8q::kNormWarpRowMaxN && N <= fp8q::kNormStreamMaxN && M >= 4 * 148 * rows &&
+         fp8q::kNormStages * rows * N * bytes <= 192 * 1024;
+}
+int norm_stream_threads(int64_t N) { return static_cast<int>(ceil_div(N / 8, 64) * 32); }
+// Blocks an SM: as many as their registers allow.
+int norm_stream_blocks(int64_t N) { return fp8q::kNormStreamThreads / norm_stream_threads(N); }
+
+// Blocks of the backward pass, and so partial rows: a function of the sizes
+// alone, so that the same call always adds in the same order.
+int64_t norm_bwd_blocks(int64_t M, int64_t N, int64_t elem) {
+  if (norm_streams(M, N, fp8q::kNormBwdRows, 2 * elem)) return 148 * norm_stream_blocks(N);
+  const NormShape s = norm_shape(N, kNormBwdOneVec);
+  const int64_t rows = s.warp_row ? 2 * (fp8q::kNormWarpRowThreads / 32) : 2;
+  const int64_t cap = 148 * (s.threads > 512 ? 1 : (s.threads > 256 ? 2 : 4));
+  const int64_t b = ceil_div(M, rows);
+  return b < cap ? b : cap;
+}
+
+template <typename T, typename W, int VPT, bool kWarpRow>
+void launch_norm(const fp8q::LayerNormArgs& a, int64_t grid, int threads, cudaStream_t s) {
+  if (a.q != nullptr)
+    fp8q::layer_norm_kernel<T, W, VPT, kWarpRow, true><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
+  else
+    fp8q::layer_norm_kernel<T, W, VPT, kWarpRow, false><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
+}
+template <typename T, typename W>
+void launch_norm_shape(const fp8q::LayerNormArgs& a, const NormShape& sh, int64_t grid, cudaStream_t s) {
+  if (sh.warp_row) {
+    if (sh.vpt == 1) launch_norm<T, W, 1, true>(a, grid, sh.threads, s);
+    else launch_norm<T, W, 2, true>(a, grid, sh.threads, s);
+  } else {
+    if (sh.vpt == 1) launch_norm<T, W, 1, false>(a, grid, sh.threads, s);
+    else launch_norm<T, W, 2, false>(a, grid, sh.threads, s);
+  }
+}
+template <typename T, typename W, bool kTiles>
+fp8q_status launch_norm_stream(const fp8q::LayerNormArgs& a, DeviceInfo* dev, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  constexpr int R = sizeof(T) == 4 ? fp8q::kNormFwdRows32 : fp8q::kNormFwdRows16;
+  constexpr int kMost = 192 * 1024;
+  auto kern = fp8q::layer_norm_stream_kernel<T, W, R, kTiles>;
+  fp8q_status st = allow_smem(kern, kMost, &done[dev - g_dev]);
+  if (st != FP8Q_OK) return st;
+  const int64_t grid = grid_for(ceil_div(a.M, R), dev->sm_count, norm_stream_blocks(a.N));
+  kern<<<static_cast<unsigned>(grid), norm_stream_threads(a.N),
+         static_cast<size_t>(fp8q::kNormStages) * R * a.N * sizeof(T), s>>>(a);
+  return launch_status();
+}
+template <typename T, typename W>
+fp8q_status launch_norm_any(const fp8q::LayerNormArgs& a, const NormShape& sh, int64_t grid, DeviceInfo* dev,
+                            cudaStream_t s) {
+  if (norm_streams(a.M, a.N, sizeof(T) == 4 ? fp8q::kNormFwdRows32 : fp8q::kNormFwdRows16, sizeof(T)))
+    return a.q != nullptr ? launch_norm_stream<T, W, true>(a, dev, s) : launch_norm_stream<T, W, false>(a, dev, s);
+  launch_norm_shape<T, W>(a, sh, grid, s);
+  return launch_status();
+}
+template <typename T, typename W>
+fp8q_status launch_norm_bwd_stream(const fp8q::LayerNormBwdArgs& a, int64_t grid, DeviceInfo* dev, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  constexpr int kRowBytes = fp8q::kNormStages * fp8q::kNormBwdRows * 2 * static_cast<int>(sizeof(T));
+  auto kern = fp8q::layer_norm_bwd_stream_kernel<T, W>;
+  fp8q_status st = allow_smem(kern, 192 * 1024, &done[dev - g_dev]);
+  if (st != FP8Q_OK) return st;
+  kern<<<static_cast<unsigned>(grid), norm_stream_threads(a.N), static_cast<size_t>(kRowBytes) * a.N, s>>>(a);
+  return launch_status();
+}
+template <typename T, typename W>
+fp8q_status launch_norm_bwd(const fp8q::LayerNormBwdArgs& a, const NormShape& sh, int64_t grid, DeviceInfo* dev,
+                            cudaStream_t s) {
+  if (norm_streams(a.M, a.N, fp8q::kNormBwdRows, 2 * sizeof(T))) return launch_norm_bwd_stream<T, W>(a, grid, dev, s);
+  const unsigned g = static_cast<unsigned>(grid);
+  if (sh.warp_row) {
+    if (sh.vpt == 1) fp8q::layer_norm_bwd_kernel<T, W, 1, true><<<g, sh.threads, 0, s>>>(a);
+    else fp8q::layer_norm_bwd_kernel<T, W, 2, true><<<g, sh.threads, 0, s>>>(a);
+  } else {
+    if (sh.vpt == 1) fp8q::layer_norm_bwd_kernel<T, W, 1, false><<<g, sh.threads, 0, s>>>(a);
+    else fp8q::layer_norm_bwd_kernel<T, W, 2, false><<<g, sh.threads, 0, s>>>(a);
+  }
+  return launch_status();
 }
 
 template <int MODE, int RT, int S>
@@ -231,18 +277,17 @@ fp8q_status fp8q_layer_norm(const void* x, int x_dtype, int64_t M, int64_t N, in
   const int64_t grid = grid_for(ceil_div(M, rows), dev->sm_count, 2048 / sh.threads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (x_dtype == FP8Q_OUT_BF16) {
-    if (param_dtype == FP8Q_OUT_BF16) launch_norm_shape<__nv_bfloat16, __nv_bfloat16>(a, sh, grid, s);
-    else launch_norm_shape<__nv_bfloat16, float>(a, sh, grid, s);
-  } else {
-    if (param_dtype == FP8Q_OUT_BF16) launch_norm_shape<float, __nv_bfloat16>(a, sh, grid, s);
-    else launch_norm_shape<float, float>(a, sh, grid, s);
+    return param_dtype == FP8Q_OUT_BF16 ? launch_norm_any<__nv_bfloat16, __nv_bfloat16>(a, sh, grid, dev, s)
+                                        : launch_norm_any<__nv_bfloat16, float>(a, sh, grid, dev, s);
   }
-  return launch_status();
+  return param_dtype == FP8Q_OUT_BF16 ? launch_norm_any<float, __nv_bfloat16>(a, sh, grid, dev, s)
+                                      : launch_norm_any<float, float>(a, sh, grid, dev, s);
 }
 
 int64_t fp8q_layer_norm_backward_workspace(int64_t M, int64_t N) {
   if (M <= 0 || N <= 0 || N > fp8q::kNormMaxN) return 0;
-  return norm_bwd_blocks(M, N) * 2 * N;
+  const int64_t b = norm_bwd_blocks(M, N, 2), f = norm_bwd_blocks(M, N, 4);     // of either type
+  return (b > f ? b : f) * 2 * N;
 }
 
 fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int x_dtype, int64_t M,
@@ -280,18 +325,18 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
   a.gamma = gamma; a.mean = mean; a.rstd = rstd; a.dx = dx; a.lddx = lddx;
   a.partial = grads ? workspace : nullptr;
   const NormShape sh = norm_shape(N, kNormBwdOneVec);
-  const int64_t grid = norm_bwd_blocks(M, N);
+  const int64_t grid = norm_bwd_blocks(M, N, elem_size(x_dtype));
   if (x_dtype == FP8Q_OUT_BF16) {
-    if (param_dtype == FP8Q_OUT_BF16) launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, sh, grid, s);
-    else launch_norm_bwd<__nv_bfloat16, float>(a, sh, grid, s);
+    st = param_dtype == FP8Q_OUT_BF16 ? launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, sh, grid, dev, s)
+                                      : launch_norm_bwd<__nv_bfloat16, float>(a, sh, grid, dev, s);
   } else {
-    if (param_dtype == FP8Q_OUT_BF16) launch_norm_bwd<float, __nv_bfloat16>(a, sh, grid, s);
-    else launch_norm_bwd<float, float>(a, sh, grid, s);
+    st = param_dtype == FP8Q_OUT_BF16 ? launch_norm_bwd<float, __nv_bfloat16>(a, sh, grid, dev, s)
+                                      : launch_norm_bwd<float, float>(a, sh, grid, dev, s);
   }
-  if ((st = launch_status()) != FP8Q_OK || !grads) return st;
-  fp8q::layer_norm_bwd_join_kernel<<<static_cast<unsigned>(ceil_div(2 * N, 32)), fp8q::kNormJoinThreads, 0, s>>>(
-      workspace, static_cast<int>(grid), a.N, dgamma, dbeta);
-  return launch_status();
+  if (st != FP8Q_OK || !grads) return st;
+  return launch_after(fp8q::layer_norm_bwd_join_kernel, dim3(static_cast<unsigned>(ceil_div(2 * N, 32))),
+                      fp8q::kNormJoinThreads, 0, s, static_cast<const float*>(workspace), static_cast<int>(grid), a.N,
+                      dgamma, dbeta);
 }
 
 int64_t fp8q_moe_few_tokens_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {

@@ -101,9 +101,6 @@ __device__ __forceinline__ const FewPlan* few_plan(const FewArgs& a) { return re
 template <typename T>
 __device__ __forceinline__ T* few_at(const FewArgs& a, int64_t off) { return reinterpret_cast<T*>(a.ws + off); }
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------
 // FP16 records: 128 values times a power of two that takes their largest
 // magnitude into [2^14, 2^15), and the inverse power.  The scaling is exact, FP16
@@ -356,7 +353,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
       const float* scale = scales + static_cast<int64_t>(row0 / 128) * KB + sc;
       const uint8_t* col = records + static_cast<int64_t>(max(now.record, 0)) * KB * kFewRecord;
       for (int c0 = 0; c0 < KB; c0 += KC) {
-        if (!warp_wait(&empty[slot], phase, abort_flag, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
+        if (!warp_wait_converged(&empty[slot], phase, abort_flag, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
         const int n = min(KC, KB - c0);
         uint8_t* stage = ring + slot * Sm::kStage;
         if (columns) {
@@ -403,7 +400,6 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   const int sw0 = ((2 * t) ^ g) * 16, sw1 = ((2 * t + 1) ^ g) * 16;
   const int col_at = KC * Sm::kChunkBytes + kc * kFewRecord;
   uint32_t slot = 0, phase = 0;
-  bool ok = true;
   for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
     float acc[TW][4];
 #pragma unroll
@@ -413,7 +409,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
     int count = 0, start = 0, row0 = 0;
     for (int st = 0; st < steps; ++st) {
       const int kb = st * KC + kc;
-      if (ok) ok = warp_wait(&full[slot], phase, abort_flag, WAIT_MMA_FULL);
+      const bool ok = warp_wait_converged(&full[slot], phase, abort_flag, WAIT_STAGE);
       if (ok && st == 0) {
         const int4 i = stage_item[slot];
         count = i.x;

@@ -42,6 +42,22 @@ struct LayerNormArgs {
   int64_t ld_sf;
 };
 
+// Programmatic dependent launch: let the next launch of the stream begin; wait
+// for the end of the launch before (and so, as every launch waits, of all before).
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A warp's wait on a barrier.  It has to leave the warp converged: called under a
+// condition the compiler cannot see to be uniform (`if (ok) ok = wait`), the warp
+// went on in two halves and issued the whole loop body twice (forward stream
+// 110 us instead of 66).  So it is called without one, and ends in a __syncwarp;
+// after a wait that gave up, the later ones return at once.
+__device__ __forceinline__ bool warp_wait_converged(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t where) {
+  const bool ok = warp_wait(bar, parity, abort, where);
+  __syncwarp();
+  return ok;
+}
+
 // Eight consecutive elements as they lie in memory (BF16: one 16-byte word,
 // FP32: two).
 template <typename T>
@@ -334,6 +350,290 @@ layer_norm_kernel(const LayerNormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Streams, for many rows of 512 < N <= 7168 whole vectors: a block per SM (more
+// where rows are short), two vectors of eight columns a thread, and a ring of
+// kNormStages stages of rows in shared memory that bulk copies fill ahead, so
+// that HBM stays busy while a step's rows are reduced.  gamma, beta and the
+// columns' gradients stay in registers for all rows of the block.  A step's rows
+// are taken out of the ring before its block barrier, which therefore also frees
+// the stage.  What bounds these kernels is the issue of instructions, most of them
+// a warp's share of the joins: hence two vectors a thread (one took 66 us for
+// the tiles of 8192 x 7168 BF16; the row kernels, which load a step's rows when
+// it begins, 84.6, and 117 backward).
+// ---------------------------------------------------------------------------
+constexpr int kNormStages = 3;
+constexpr int kNormStreamThreads = 448;                    // up to 144 registers each
+constexpr int kNormStreamMaxN = 16 * kNormStreamThreads;
+constexpr int kNormFwdRows16 = 4, kNormFwdRows32 = 2;      // rows a step, BF16 and FP32
+constexpr int kNormBwdRows = 2;                            // of x and of dy
+
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float2 (&f)[4]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16lo(u[i]), bf16hi(u[i]));
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float2 (&f)[4]) {
+  f[0] = f2u(r.w[0].x, r.w[0].y);
+  f[1] = f2u(r.w[0].z, r.w[0].w);
+  f[2] = f2u(r.w[1].x, r.w[1].y);
+  f[3] = f2u(r.w[1].z, r.w[1].w);
+}
+__device__ __forceinline__ void pack8(Raw8<__nv_bfloat16>& r, const float2 (&f)[4]) {
+  r.w[0] = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ void pack8(Raw8<float>& r, const float2 (&f)[4]) {
+  r.w[0] = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+  r.w[1] = make_uint4(__float_as_uint(f[2].x), __float_as_uint(f[2].y), __float_as_uint(f[3].x), __float_as_uint(f[3].y));
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float sum8(const float2 (&f)[4]) {
+  const float2 s = fadd2(fadd2(f[0], f[1]), fadd2(f[2], f[3]));
+  return s.x + s.y;
+}
+// Sum over 32 lanes of R values (2 or 4): lanes (32 / R) i .. end with that of value i.
+template <int R>
+__device__ __forceinline__ float warp_sum_rows(const float (&v)[R], int lane) {
+  if constexpr (R == 2) return warp_sum2(v[0], v[1], lane);
+  else return warp_sum4(v[0], v[1], v[2], v[3], lane);
+}
+// Sum over the 32 / R lanes that share a row.
+template <int R>
+__device__ __forceinline__ float row_lanes_sum(float v) {
+#pragma unroll
+  for (int o = 16 / R; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// x / n, correctly rounded, with inv = fl(1 / n): a product and one correction
+// step of Markstein's division (see e4m3x2_neg_quot).
+__device__ __forceinline__ float div_by(float x, float n, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, n, x), inv, q);
+}
+
+// What a thread, a warp and a row of a stream hold: two vectors a thread, t and
+// t + T of the row's N / 8.
+struct NormStream {
+  int N, t, lane, warp, warps;
+  bool mine[2];
+  float n, inv_n;          // of the row
+  float n_w, inv_nw;       // of this warp
+  float inv_nt;            // of this thread
+  __device__ __forceinline__ explicit NormStream(int N_) : N(N_) {
+    t = threadIdx.x;
+    lane = t & 31;
+    warp = t >> 5;
+    warps = blockDim.x >> 5;
+    mine[0] = 8 * t < N;
+    mine[1] = 8 * (t + static_cast<int>(blockDim.x)) < N;
+    n = static_cast<float>(N);
+    inv_n = __frcp_rn(n);
+    n_w = count(warp);
+    inv_nw = __frcp_rn(fmaxf(n_w, 1.0f));
+    inv_nt = mine[1] ? 0.0625f : 0.125f;
+  }
+  __device__ __forceinline__ float count(int w) const {      // of warp w
+    return w < warps ? static_cast<float>(norm_warp_count<2>(N, w, warps)) : 0.0f;
+  }
+  __device__ __forceinline__ int vec(int i) const { return t + i * static_cast<int>(blockDim.x); }
+};
+
+template <typename T>
+__device__ __forceinline__ void stream_read(Raw8<T>& r, const uint8_t* row, int vec, bool live) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    r.w[i] = live ? reinterpret_cast<const uint4*>(row + vec * 8 * sizeof(T))[i] : make_uint4(0, 0, 0, 0);
+}
+template <typename W>
+__device__ __forceinline__ void stream_param(float2 (&p)[4], const void* src, int vec, bool live, float none) {
+  float f[8];
+  load_param8<W>(f, src, vec, live ? 8 : 0, none);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = make_float2(f[2 * j], f[2 * j + 1]);
+}
+
+template <typename T, typename W, int R, bool kTiles>
+__global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kernel(const LayerNormArgs a) {
+  constexpr int kL = 32 / R;                     // lanes that share a row in the warps' joins
+  constexpr int kJoin = (kNormStreamThreads / 32 + kL - 1) / kL;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 part[2][32][R];
+  __shared__ __align__(8) uint64_t full[kNormStages];
+  __shared__ int abort_flag;
+  const NormStream c(a.N);
+  const int t = c.t, lane = c.lane;
+  const uint32_t row_bytes = a.N * sizeof(T);
+  const int64_t steps = (a.M + R - 1) / R;
+  if (t == 0) {
+#pragma unroll
+    for (int s = 0; s < kNormStages; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  uint32_t issued = 0;
+  auto request = [&](int64_t step, int s) {      // thread 0
+    const int64_t row0 = step * R;
+    const int rows = static_cast<int>(a.M - row0 < R ? a.M - row0 : R);
+    ++issued;
+    mbar_arrive_expect_tx(&full[s], rows * row_bytes);
+    for (int r = 0; r < rows; ++r)
+      bulk_load(smem + (s * R + r) * row_bytes, static_cast<const T*>(a.x) + (row0 + r) * a.ldx, row_bytes, &full[s]);
+  };
+  if (t == 0) {
+    int s = 0;
+    for (int64_t step = blockIdx.x; step < steps && s < kNormStages; step += gridDim.x, ++s) request(step, s);
+  }
+  float2 ga[2][4], be[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    stream_param<W>(ga[i], a.gamma, c.vec(i), c.mine[i], 1.0f);
+    stream_param<W>(be[i], a.beta, c.vec(i), c.mine[i], 0.0f);
+  }
+  // the warps whose parts this lane joins: of row lane / kL
+  float count[kJoin];
+#pragma unroll
+  for (int k = 0; k < kJoin; ++k) count[k] = c.count(lane % kL + kL * k);
+  int stage = 0, parity = 0;
+  uint32_t phase = 0;
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x, parity ^= 1) {
+    warp_wait_converged(&full[stage], phase, &abort_flag, WAIT_STAGE);
+    Raw8<T> raw[R][2];
+    float sum[R], m2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // the thread's sum, and its deviations from its own mean
+      float2 f[2][4], q = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        stream_read(raw[r][i], smem + (stage * R + r) * row_bytes, c.vec(i), c.mine[i]);
+        unpack8(raw[r][i], f[i]);
+      }
+      sum[r] = sum8(f[0]) + sum8(f[1]);
+      const float2 m = f2(-c.inv_nt * sum[r]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (c.mine[i]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 d = fadd2(f[i][j], m);
+            q = ffma2(d, d, q);
+          }
+        }
+      }
+      m2[r] = q.x + q.y;
+    }
+    // the warp's: the deviations add up to the threads' own and those of their means
+    const float wsum = warp_sum_rows<R>(sum, lane);
+    const float wmean = div_by(wsum, fmaxf(c.n_w, 1.0f), c.inv_nw);
+    const float n_t = c.mine[1] ? 16.0f : (c.mine[0] ? 8.0f : 0.0f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float d = fmaf(c.inv_nt, sum[r], -__shfl_sync(0xFFFFFFFFu, wmean, r * kL));
+      m2[r] = fmaf(n_t * d, d, m2[r]);
+    }
+    const float wm2 = warp_sum_rows<R>(m2, lane);
+    if (lane % kL == 0) part[parity][c.warp][lane / kL] = make_float2(wmean, wm2);
+    __syncthreads();
+    // the stage has been read by all: request the step that comes into it
+    if (t == 0 && step + kNormStages * gridDim.x < steps) {
+      fence_proxy_async_shared();
+      request(step + kNormStages * gridDim.x, stage);
+    }
+    if (++stage == kNormStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    // the row's, in the same way from the warps
+    float2 p[kJoin];
+    float total = 0.0f, dev = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const int w = lane % kL + kL * k;
+      p[k] = w < c.warps ? part[parity][w][lane / kL] : make_float2(0.0f, 0.0f);
+      total = fmaf(count[k], p[k].x, total);
+    }
+    const float mean_l = div_by(row_lanes_sum<R>(total), c.n, c.inv_n);
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const float d = p[k].x - mean_l;
+      dev += fmaf(count[k] * d, d, p[k].y);
+    }
+    const float rstd_l = rsqrtf(div_by(row_lanes_sum<R>(dev), c.n, c.inv_n) + a.eps);
+    const int64_t row0 = step * R;
+    if (c.warp == 0 && lane % kL == 0 && row0 + lane / kL < a.M) {
+      if (a.mean != nullptr) a.mean[row0 + lane / kL] = mean_l;
+      if (a.rstd != nullptr) a.rstd[row0 + lane / kL] = rstd_l;
+    }
+#pragma unroll
+    for (int r0 = 0; r0 < R; r0 += 2) {          // two rows, and so four tiles, at a time
+      float2 y[2][2][4];
+      float amax[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = r0 + u;
+        const float2 m = f2(-__shfl_sync(0xFFFFFFFFu, mean_l, r * kL)), k = f2(__shfl_sync(0xFFFFFFFFu, rstd_l, r * kL));
+        const bool live = row0 + r < a.M;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float2 (&f)[4] = y[u][i];
+          unpack8(raw[r][i], f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = ffma2(fmul2(fadd2(f[j], m), k), ga[i][j], be[i][j]);
+          if (a.y != nullptr && c.mine[i] && live && chk(8 * c.vec(i) + 7, a.ldy, CHK_NORM)) {
+            Raw8<T> o;
+            pack8(o, f);
+            store8(static_cast<T*>(a.y) + (row0 + r) * a.ldy + 8 * c.vec(i), o, 8);
+          }
+          if (kTiles) {
+            float m4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m4[j] = fmaxf(fabsf(f[j].x), fabsf(f[j].y));
+            amax[2 * u + i] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+        }
+      }
+      if constexpr (kTiles) {
+        // the four tiles' maxima over 16 lanes: lanes 4 i .. 4 i + 3 of the 16 end
+        // with that of tile i = 2 (row) + (vector), and so its scale
+        const bool up = (lane & 8) != 0, up2 = (lane & 4) != 0;
+        const float k0 = fmaxf(up ? amax[2] : amax[0], __shfl_xor_sync(0xFFFFFFFFu, up ? amax[0] : amax[2], 8));
+        const float k1 = fmaxf(up ? amax[3] : amax[1], __shfl_xor_sync(0xFFFFFFFFu, up ? amax[1] : amax[3], 8));
+        float m = fmaxf(up2 ? k1 : k0, __shfl_xor_sync(0xFFFFFFFFu, up2 ? k0 : k1, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        const float s_l = tile_scale(m);
+        const float nr_l = -__frcp_rn(s_l);
+        const int64_t own = row0 + r0 + (up ? 1 : 0);
+        if ((lane & 3) == 0 && (up2 ? c.mine[1] : c.mine[0]) && own < a.M && chk(own, a.ld_sf, CHK_Q1_SF))
+          a.sf[(c.vec(up2 ? 1 : 0) >> 4) * a.ld_sf + own] = s_l;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int from = (lane & 16) + 4 * (2 * u + i);
+            const float s = __shfl_sync(0xFFFFFFFFu, s_l, from), nr = __shfl_sync(0xFFFFFFFFu, nr_l, from);
+            const float2 (&f)[4] = y[u][i];
+            // y is an FP32 value here: see the row kernel
+            uint32_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = e4m3x2_neg_quot(f[j].x, f[j].y, nr, nr, s, s);
+            uint2 o;
+            o.x = (q[0] | (q[1] << 16)) ^ kFlipSigns;
+            o.y = (q[2] | (q[3] << 16)) ^ kFlipSigns;
+            if (c.mine[i] && row0 + r0 + u < a.M && chk(8 * c.vec(i) + 7, a.ldq, CHK_Q1))
+              *reinterpret_cast<uint2*>(a.q + (row0 + r0 + u) * a.ldq + 8 * c.vec(i)) = o;
+          }
+      }
+    }
+  }
+  // a wait that gave up leaves copies in flight, which still write this block's memory
+  for (uint32_t j = issued > kNormStages ? issued - kNormStages : 0; j < issued; ++j)
+    mbar_wait(&full[j % kNormStages], (j / kNormStages) & 1, nullptr, WAIT_DRAIN, 1ll << 22);
+}
+
+// ---------------------------------------------------------------------------
 // Backward.  Row groups as in the forward pass, two rows at a time; mean and
 // rstd come from it.  The two row sums of both rows are one four-value warp
 // reduction and one barrier.  Each thread keeps its columns' dgamma and dbeta
@@ -369,6 +669,7 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (kWarpRow ? kNormWarpRowThreads / 32 : 1);
   const int N = a.N;
   const float inv_n = 1.0f / static_cast<float>(N);
+  pdl_launch();
   float dga[VPT][8], dbe[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
@@ -493,6 +794,158 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
   }
 }
 
+// The backward pass as a stream: a stage holds kNormBwdRows rows of x and of dy.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_kernel(const LayerNormBwdArgs a) {
+  constexpr int R = kNormBwdRows;
+  constexpr int kJoin = (kNormStreamThreads / 32 + 7) / 8;
+  static_assert(R == 2, "two sums of two rows: a four-value reduction");
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float part[2][32][4];
+  __shared__ __align__(8) uint64_t full[kNormStages];
+  __shared__ int abort_flag;
+  const NormStream c(a.N);
+  const int t = c.t, lane = c.lane;
+  const uint32_t row_bytes = a.N * sizeof(T);
+  const int64_t steps = (a.M + R - 1) / R;
+  pdl_launch();
+  if (t == 0) {
+#pragma unroll
+    for (int s = 0; s < kNormStages; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  uint32_t issued = 0;
+  auto request = [&](int64_t step, int s) {      // thread 0
+    const int64_t row0 = step * R;
+    const int rows = static_cast<int>(a.M - row0 < R ? a.M - row0 : R);
+    ++issued;
+    mbar_arrive_expect_tx(&full[s], 2 * rows * row_bytes);
+    for (int r = 0; r < rows; ++r) {
+      uint8_t* dst = smem + (s * R + r) * 2 * row_bytes;
+      bulk_load(dst, static_cast<const T*>(a.x) + (row0 + r) * a.ldx, row_bytes, &full[s]);
+      bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + (row0 + r) * a.lddy, row_bytes, &full[s]);
+    }
+  };
+  if (t == 0) {
+    int s = 0;
+    for (int64_t step = blockIdx.x; step < steps && s < kNormStages; step += gridDim.x, ++s) request(step, s);
+  }
+  float2 ga[2][4], dga[2][4], dbe[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    stream_param<W>(ga[i], a.gamma, c.vec(i), c.mine[i], 1.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dga[i][j] = dbe[i][j] = f2(0.0f);
+  }
+  // the statistics of a step's rows, a step ahead (a row past the end takes those of the step's first)
+  float mean_next[R], rstd_next[R];
+  auto statistics = [&](int64_t step) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = step * R + r < a.M ? step * R + r : step * R;
+      mean_next[r] = step < steps ? __ldg(a.mean + row) : 0.0f;
+      rstd_next[r] = step < steps ? __ldg(a.rstd + row) : 0.0f;
+    }
+  };
+  statistics(blockIdx.x);
+  int stage = 0, parity = 0;
+  uint32_t phase = 0;
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x, parity ^= 1) {
+    const int64_t row0 = step * R;
+    float2 mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = f2(-mean_next[r]);
+      rstd[r] = f2(rstd_next[r]);
+    }
+    statistics(step + gridDim.x);
+    warp_wait_converged(&full[stage], phase, &abort_flag, WAIT_STAGE);
+    Raw8<T> rx[R][2], rd[R][2];
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint8_t* src = smem + (stage * R + r) * 2 * row_bytes;
+      const bool live = row0 + r < a.M;          // what lies past the end counts as zero
+      float2 s1 = f2(0.0f), s2 = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        stream_read(rx[r][i], src, c.vec(i), c.mine[i] && live);
+        stream_read(rd[r][i], src + row_bytes, c.vec(i), c.mine[i] && live);
+        float2 x[4], d[4];
+        unpack8(rx[r][i], x);
+        unpack8(rd[r][i], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 xh = fmul2(fadd2(x[j], mean[r]), rstd[r]), g = fmul2(d[j], ga[i][j]);
+          s1 = fadd2(s1, g);
+          s2 = ffma2(g, xh, s2);
+          dga[i][j] = ffma2(d[j], xh, dga[i][j]);
+          dbe[i][j] = fadd2(dbe[i][j], d[j]);
+        }
+      }
+      v[2 * r] = s1.x + s1.y;
+      v[2 * r + 1] = s2.x + s2.y;
+    }
+    const float ws = warp_sum4(v[0], v[1], v[2], v[3], lane);
+    if ((lane & 7) == 0) part[parity][c.warp][lane >> 3] = ws;
+    __syncthreads();
+    if (t == 0 && step + kNormStages * gridDim.x < steps) {
+      fence_proxy_async_shared();
+      request(step + kNormStages * gridDim.x, stage);
+    }
+    if (++stage == kNormStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    float tot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const int w = (lane & 7) + 8 * k;
+      if (w < c.warps) tot += part[parity][w][lane >> 3];
+    }
+    tot = row_lanes_sum<4>(tot) * c.inv_n;
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 c1 = f2(-__shfl_sync(0xFFFFFFFFu, tot, 16 * r)), c2 = f2(-__shfl_sync(0xFFFFFFFFu, tot, 16 * r + 8));
+        const bool live = row0 + r < a.M;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float2 x[4], d[4];
+          unpack8(rx[r][i], x);
+          unpack8(rd[r][i], d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 xh = fmul2(fadd2(x[j], mean[r]), rstd[r]);
+            d[j] = fmul2(rstd[r], ffma2(xh, c2, ffma2(d[j], ga[i][j], c1)));
+          }
+          if (c.mine[i] && live && chk(8 * c.vec(i) + 7, a.lddx, CHK_NORM)) {
+            Raw8<T> o;
+            pack8(o, d);
+            store8(static_cast<T*>(a.dx) + (row0 + r) * a.lddx + 8 * c.vec(i), o, 8);
+          }
+        }
+      }
+    }
+  }
+  // a wait that gave up leaves copies in flight, which still write this block's memory
+  for (uint32_t j = issued > kNormStages ? issued - kNormStages : 0; j < issued; ++j)
+    mbar_wait(&full[j % kNormStages], (j / kNormStages) & 1, nullptr, WAIT_DRAIN, 1ll << 22);
+  if (a.partial == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!c.mine[i]) continue;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.N + 8 * c.vec(i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *reinterpret_cast<float2*>(out + 2 * j) = dga[i][j];
+      *reinterpret_cast<float2*>(out + a.N + 2 * j) = dbe[i][j];
+    }
+  }
+}
+
 // dgamma[c], dbeta[c] <- the sum over `rows` partial rows: 32 columns a block,
 // 32 threads a column, then a fixed tree.
 constexpr int kNormJoinThreads = 1024;
@@ -502,6 +955,7 @@ layer_norm_bwd_join_kernel(const float* __restrict__ partial, int rows, int N, f
   __shared__ float s[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;               // of 2 N columns: dgamma's, then dbeta's
+  pdl_wait();
   float v = 0.0f;
   if (c < 2 * N)
     for (int r = ry; r < rows; r += 32) v += partial[static_cast<int64_t>(r) * 2 * N + c];

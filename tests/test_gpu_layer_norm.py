@@ -194,3 +194,60 @@ def test_captured_and_replayed(fp8q):
     y2, mean2, rstd2 = fp8q.layer_norm(x, gamma, beta)
     assert torch.equal(y, y2) and torch.equal(rstd, rstd2)
     assert all(torch.equal(a, b) for a, b in zip(out, fp8q.layer_norm_backward(dy, x, gamma, mean, rstd)))
+
+
+# many rows: the kernels that stream rows through shared memory, at widths of one and of many blocks an SM, whole and
+# odd row counts, and just outside their range
+STREAMS = [(2368, 7168), (2371, 520), (4801, 1024), (2400, 4096), (2369, 4104), (2500, 7176), (2367, 1280), (2401, 1027)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", STREAMS)
+def test_many_rows(fp8q, M, N, dtype):
+    gamma, beta = params(N, "f32", 7 * N + M)
+    check_forward(fp8q, make(M, N, dtype, M + N), gamma, beta)
+    check_backward(fp8q, M, N, dtype, gamma)
+
+
+@pytest.mark.parametrize("which", ["none", "bf16"])
+def test_many_rows_parameters(fp8q, which):
+    gamma, beta = (None, None) if which == "none" else params(2048, "bf16", 1)
+    check_forward(fp8q, make(2400, 2048, "bf16", 1), gamma, beta)
+    check_forward(fp8q, make(2400, 2048, "f32", 1, offset=2000.0, scale=0.5), gamma, beta)
+    check_backward(fp8q, 2400, 2048, "bf16", gamma)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(2370, 7168), (2369, 640), (2368, 1152)])
+def test_many_rows_tiles(fp8q, M, N, dtype):
+    """The stream's tiles equal those of the same rows in short calls, code for code and scale for scale, up to
+    quotients and scales that their statistics' roundings (another order of the same sums) put on the other side of a
+    border: within the bounds of y."""
+    x = make(M, N, dtype, N)
+    gamma, beta = params(N, "f32", N)
+    q, sf, mean, rstd, y = fp8q.layer_norm_quant(x, gamma, beta, EPS, keep_y=True)
+    want, _, wr, xh = R.layer_norm(x, gamma, beta, EPS)
+    e = R.layer_norm_bound(x, gamma, beta, wr, xh)
+    tol = e + R.half_step(x.dtype) * (want.abs() + e)
+    assert ((y.double() - want).abs() <= tol).all()
+    s = sf[:, :M].t().double()
+    s_want = (want.abs().view(M, -1, 128).amax(2) / 448).clamp_min(1e-12)
+    assert ((s - s_want).abs() <= e.view(M, -1, 128).amax(2) / 448 + 2 * R.U * s_want).all()
+    dec = q.view(torch.float8_e4m3fn).double().view(M, -1, 128) * s[:, :, None]
+    y64 = want.view(M, -1, 128)
+    step = torch.maximum(y64.abs() * 2.0 ** -4, s[:, :, None] * 2.0 ** -10)
+    assert ((dec - y64).abs() <= step * (1 + 2.0 ** -10) + 2 * e.view(M, -1, 128)).all()
+    only = fp8q.layer_norm_quant(x, gamma, beta, EPS)
+    assert torch.equal(only[0], q) and torch.equal(only[1][:, :M], sf[:, :M]) and torch.equal(only[3], rstd)
+
+
+def test_many_rows_write_only_the_rows(fp8q):
+    N, M, ld = 1000, 2400, 1024
+    x = make(M, N, "bf16", 5, pad=16)
+    y = torch.full((M + 2, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8q.fp8q_layer_norm(x, None, None, EPS, y[:M, :N])
+    assert torch.all(y[:, N:] == 7.0) and torch.all(y[M:] == 7.0) and torch.equal(y[:M, :N], fp8q.layer_norm(x)[0])
+    dx = torch.full((M + 2, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, mean, rstd = fp8q.layer_norm(x)
+    fp8q.fp8q_layer_norm_backward(x, x, None, mean, rstd, dx[:M, :N])
+    assert torch.all(dx[:, N:] == 7.0) and torch.all(dx[M:] == 7.0)
