@@ -354,9 +354,10 @@ layer_norm_kernel(const LayerNormArgs a) {
 // where rows are short), two vectors of eight columns a thread, and a ring of
 // kNormStages stages of rows in shared memory that bulk copies fill ahead, so
 // that HBM stays busy while a step's rows are reduced.  gamma, beta and the
-// columns' gradients stay in registers for all rows of the block.  A step's rows
-// are taken out of the ring before its block barrier, which therefore also frees
-// the stage.  What bounds these kernels is the issue of instructions, most of them
+// columns' gradients stay in registers for all rows of the block; the rows are
+// read from the ring twice, for the sums and for the outputs, rather than kept in
+// registers (backward 90 us instead of 94: no spills).  A step's block barrier
+// also tells that the step before is done with its stage.  What bounds these kernels is the issue of instructions, most of them
 // a warp's share of the joins: hence two vectors a thread (one took 66 us for
 // the tiles of 8192 x 7168 BF16; the row kernels, which load a step's rows when
 // it begins, 84.6, and 117 backward).
@@ -499,7 +500,6 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
   uint32_t phase = 0;
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x, parity ^= 1) {
     warp_wait_converged(&full[stage], phase, &abort_flag, WAIT_STAGE);
-    Raw8<T> raw[R][2];
     float sum[R], m2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -507,8 +507,9 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
       float2 f[2][4], q = f2(0.0f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        stream_read(raw[r][i], smem + (stage * R + r) * row_bytes, c.vec(i), c.mine[i]);
-        unpack8(raw[r][i], f[i]);
+        Raw8<T> raw;
+        stream_read(raw, smem + (stage * R + r) * row_bytes, c.vec(i), c.mine[i]);
+        unpack8(raw, f[i]);
       }
       sum[r] = sum8(f[0]) + sum8(f[1]);
       const float2 m = f2(-c.inv_nt * sum[r]);
@@ -536,11 +537,13 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
     const float wm2 = warp_sum_rows<R>(m2, lane);
     if (lane % kL == 0) part[parity][c.warp][lane / kL] = make_float2(wmean, wm2);
     __syncthreads();
-    // the stage has been read by all: request the step that comes into it
-    if (t == 0 && step + kNormStages * gridDim.x < steps) {
+    // all are done with the stage of the step before: request the step that comes into it
+    const int64_t coming = step + (kNormStages - 1) * static_cast<int64_t>(gridDim.x);
+    if (t == 0 && step > blockIdx.x && coming < steps) {
       fence_proxy_async_shared();
-      request(step + kNormStages * gridDim.x, stage);
+      request(coming, stage > 0 ? stage - 1 : kNormStages - 1);
     }
+    const uint8_t* rows_at = smem + stage * R * row_bytes;
     if (++stage == kNormStages) {
       stage = 0;
       phase ^= 1;
@@ -578,7 +581,9 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float2 (&f)[4] = y[u][i];
-          unpack8(raw[r][i], f);
+          Raw8<T> raw;
+          stream_read(raw, rows_at + r * row_bytes, c.vec(i), c.mine[i]);
+          unpack8(raw, f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) f[j] = ffma2(fmul2(fadd2(f[j], m), k), ga[i][j], be[i][j]);
           if (a.y != nullptr && c.mine[i] && live && chk(8 * c.vec(i) + 7, a.ldy, CHK_NORM)) {
@@ -862,7 +867,6 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
     }
     statistics(step + gridDim.x);
     warp_wait_converged(&full[stage], phase, &abort_flag, WAIT_STAGE);
-    Raw8<T> rx[R][2], rd[R][2];
     float v[4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -871,11 +875,12 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
       float2 s1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        stream_read(rx[r][i], src, c.vec(i), c.mine[i] && live);
-        stream_read(rd[r][i], src + row_bytes, c.vec(i), c.mine[i] && live);
+        Raw8<T> rx, rd;
+        stream_read(rx, src, c.vec(i), c.mine[i] && live);
+        stream_read(rd, src + row_bytes, c.vec(i), c.mine[i] && live);
         float2 x[4], d[4];
-        unpack8(rx[r][i], x);
-        unpack8(rd[r][i], d);
+        unpack8(rx, x);
+        unpack8(rd, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 xh = fmul2(fadd2(x[j], mean[r]), rstd[r]), g = fmul2(d[j], ga[i][j]);
@@ -891,10 +896,12 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
     const float ws = warp_sum4(v[0], v[1], v[2], v[3], lane);
     if ((lane & 7) == 0) part[parity][c.warp][lane >> 3] = ws;
     __syncthreads();
-    if (t == 0 && step + kNormStages * gridDim.x < steps) {
+    const int64_t coming = step + (kNormStages - 1) * static_cast<int64_t>(gridDim.x);
+    if (t == 0 && step > blockIdx.x && coming < steps) {
       fence_proxy_async_shared();
-      request(step + kNormStages * gridDim.x, stage);
+      request(coming, stage > 0 ? stage - 1 : kNormStages - 1);
     }
+    const uint8_t* rows_at = smem + stage * R * 2 * row_bytes;
     if (++stage == kNormStages) {
       stage = 0;
       phase ^= 1;
@@ -913,9 +920,13 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
         const bool live = row0 + r < a.M;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          Raw8<T> rx, rd;
+          const uint8_t* src = rows_at + r * 2 * row_bytes;
+          stream_read(rx, src, c.vec(i), c.mine[i] && live);
+          stream_read(rd, src + row_bytes, c.vec(i), c.mine[i] && live);
           float2 x[4], d[4];
-          unpack8(rx[r][i], x);
-          unpack8(rd[r][i], d);
+          unpack8(rx, x);
+          unpack8(rd, d);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 xh = fmul2(fadd2(x[j], mean[r]), rstd[r]);
