@@ -224,24 +224,50 @@ fp8q_status launch_lora_shrink(const fp8q::LoraArgs& a, const LoraShape& sh, Dev
   return launch_status();
 }
 
-template <typename T, int KQ, int MB, int CB>
-fp8q_status launch_lora_expand(const fp8q::LoraArgs& a, DeviceInfo* dev, cudaStream_t s) {
-  const int64_t blocks = ceil_div(a.T, 16 * MB) + (a.groups < a.T ? a.groups : a.T);
-  const int64_t grid = grid_for(blocks * ceil_div(a.N, 256 * CB), dev->sm_count, 4);
-  fp8q::lora_expand_kernel<T, KQ, MB, CB><<<static_cast<unsigned>(grid), fp8q::kLoraThreads, 0, s>>>(a);
+template <typename T, int KQ, int MB, int S, int WARPS>
+fp8q_status launch_lora_expand(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  using Sm = fp8q::LoraExpandSmem<T, KQ, MB, S, WARPS>;
+  auto kern = fp8q::lora_expand_kernel<T, KQ, MB, S, WARPS>;
+  constexpr int kThreads = 32 * WARPS;
+  fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
+  if (st != FP8Q_OK) return st;
+  const int per_sm = Sm::kBytes + static_cast<int>(sizeof(fp8q::LoraGroups)) + 1024 <= 113 * 1024 ? 2 : 1;
+  int64_t blocks = a.T / (16 * MB) + (a.groups < a.T ? a.groups : a.T);
+  if (blocks > a.T) blocks = a.T;
+  // up to eight units of columns an item, while two items a resident block remain
+  const int64_t units = blocks * ceil_div(a.N, kThreads);
+  int64_t n = units / (2 * per_sm * static_cast<int64_t>(dev->sm_count));
+  a.col_units = static_cast<int>(n < 1 ? 1 : (n > 8 ? 8 : n));
+  const int64_t grid = grid_for(blocks * ceil_div(ceil_div(a.N, kThreads), a.col_units), dev->sm_count, per_sm);
+  if (after_shrink) return launch_after(kern, dim3(static_cast<unsigned>(grid)), kThreads, Sm::kBytes, s, a);
+  kern<<<static_cast<unsigned>(grid), kThreads, Sm::kBytes, s>>>(a);
+  return launch_status();
+}
+template <typename T, int TOKENS>
+fp8q_status lora_expand_few(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev, cudaStream_t s) {
+  constexpr int kPerSm = TOKENS > 2 ? 2 : 4;
+  auto kern = fp8q::lora_expand_few_kernel<T, TOKENS>;
+  int64_t blocks = a.T / TOKENS + (a.groups < a.T ? a.groups : a.T);
+  if (blocks > a.T) blocks = a.T;
+  // an item costs some 3 us before its first column (its group, tokens and v): as few as fill the SMs
+  const int64_t units = ceil_div(a.N, fp8q::kLoraFewColumns);
+  const int64_t n = ceil_div(blocks * units, kPerSm * static_cast<int64_t>(dev->sm_count));
+  a.col_units = static_cast<int>(n > 16 ? 16 : n);
+  const int64_t grid = grid_for(blocks * ceil_div(units, a.col_units), dev->sm_count, kPerSm);
+  if (after_shrink)
+    return launch_after(kern, dim3(static_cast<unsigned>(grid)), fp8q::kLoraThreads, 0, s, a);
+  kern<<<static_cast<unsigned>(grid), fp8q::kLoraThreads, 0, s>>>(a);
   return launch_status();
 }
 template <typename T>
 fp8q_status lora_expand(const fp8q::LoraArgs& a, bool many, DeviceInfo* dev, cudaStream_t s) {
-  if (!many) {
-    if (a.r <= 32) return launch_lora_expand<T, 1, 1, 4>(a, dev, s);
-    if (a.r <= 64) return launch_lora_expand<T, 2, 1, 4>(a, dev, s);
-    return launch_lora_expand<T, 4, 1, 4>(a, dev, s);
-  }
-  constexpr int kMB = sizeof(T) == 4 ? 2 : 4;
-  if (a.r <= 32) return launch_lora_expand<T, 1, kMB, 2>(a, dev, s);
-  if (a.r <= 64) return launch_lora_expand<T, 2, kMB, 2>(a, dev, s);
-  return launch_lora_expand<T, 4, 2, 2>(a, dev, s);
+  constexpr bool kF32 = sizeof(T) == 4;
+  const bool after = a.adapters > 0;
+  if (!many) return a.T <= 2 * a.groups ? lora_expand_few<T, 2>(a, after, dev, s) : lora_expand_few<T, 8>(a, after, dev, s);
+  if (a.r <= 32) return launch_lora_expand<T, 1, 2, 2, 16>(a, after, dev, s);
+  if (a.r <= 64) return launch_lora_expand<T, 2, kF32 ? 1 : 2, 2, 16>(a, after, dev, s);
+  return launch_lora_expand<T, 4, kF32 ? 1 : 2, 2, 8>(a, after, dev, s);
 }
 
 }  // namespace
