@@ -224,6 +224,23 @@ fp8q_status launch_lora_shrink(const fp8q::LoraArgs& a, const LoraShape& sh, Dev
   return launch_status();
 }
 
+// Units of columns an item of the expansion takes: the split of a block's `units`
+// with the least rounds x (units + overhead) over the resident blocks; an item
+// costs some 3 us before its first column (its group, tokens and v), which is
+// `overhead` units.
+int lora_col_units(int64_t blocks, int64_t units, int64_t resident, int64_t overhead) {
+  int64_t best = units, cost = -1;
+  for (int64_t parts = 1; parts <= units && parts <= 64; ++parts) {
+    const int64_t u = ceil_div(units, parts);
+    const int64_t c = ceil_div(blocks * ceil_div(units, u), resident) * (u + overhead);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = u;
+    }
+  }
+  return static_cast<int>(best);
+}
+
 template <typename T, int KQ, int MB, int S, int WARPS>
 fp8q_status launch_lora_expand(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
@@ -235,10 +252,7 @@ fp8q_status launch_lora_expand(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* 
   const int per_sm = Sm::kBytes + static_cast<int>(sizeof(fp8q::LoraGroups)) + 1024 <= 113 * 1024 ? 2 : 1;
   int64_t blocks = a.T / (16 * MB) + (a.groups < a.T ? a.groups : a.T);
   if (blocks > a.T) blocks = a.T;
-  // up to eight units of columns an item, while two items a resident block remain
-  const int64_t units = blocks * ceil_div(a.N, kThreads);
-  int64_t n = units / (2 * per_sm * static_cast<int64_t>(dev->sm_count));
-  a.col_units = static_cast<int>(n < 1 ? 1 : (n > 8 ? 8 : n));
+  a.col_units = lora_col_units(blocks, ceil_div(a.N, kThreads), static_cast<int64_t>(per_sm) * dev->sm_count, 1);
   const int64_t grid = grid_for(blocks * ceil_div(ceil_div(a.N, kThreads), a.col_units), dev->sm_count, per_sm);
   if (after_shrink) return launch_after(kern, dim3(static_cast<unsigned>(grid)), kThreads, Sm::kBytes, s, a);
   kern<<<static_cast<unsigned>(grid), kThreads, Sm::kBytes, s>>>(a);
@@ -250,10 +264,8 @@ fp8q_status lora_expand_few(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev
   auto kern = fp8q::lora_expand_few_kernel<T, TOKENS>;
   int64_t blocks = a.T / TOKENS + (a.groups < a.T ? a.groups : a.T);
   if (blocks > a.T) blocks = a.T;
-  // an item costs some 3 us before its first column (its group, tokens and v): as few as fill the SMs
   const int64_t units = ceil_div(a.N, fp8q::kLoraFewColumns);
-  const int64_t n = ceil_div(blocks * units, kPerSm * static_cast<int64_t>(dev->sm_count));
-  a.col_units = static_cast<int>(n > 16 ? 16 : n);
+  a.col_units = lora_col_units(blocks, units, static_cast<int64_t>(kPerSm) * dev->sm_count, 2);
   const int64_t grid = grid_for(blocks * ceil_div(units, a.col_units), dev->sm_count, kPerSm);
   if (after_shrink)
     return launch_after(kern, dim3(static_cast<unsigned>(grid)), fp8q::kLoraThreads, 0, s, a);
