@@ -141,6 +141,9 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
 // reads back only what it copied itself (cp.async), so the ring of S units (one
 // unit: one chunk of one item) needs no barrier, and runs on across items.
 // ---------------------------------------------------------------------------
+struct LoraTrue { static constexpr bool value = true; };
+struct LoraFalse { static constexpr bool value = false; };
+
 template <int RT, int G, int P, int S>
 struct LoraSmem {
   static constexpr int kUnit = P * (2 * RT + G) * 512;
@@ -250,28 +253,31 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
   int slot = 0;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const Where w = where(item);
-    float acc[RT][G][4];
+    // Sums of 64 products come from the tensor cores (2 / P chunks of 32 P), then an FP32 addition.
+    float2 acc[RT][G][2];
+    float part[RT][G][4];
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
-      for (int j = 0; j < G; ++j)
+      for (int j = 0; j < G; ++j) acc[m][j][0] = acc[m][j][1] = f2(0.0f);
+    auto promote = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
-    for (int chunk = w.chunk0 + warp; chunk < w.chunk1; chunk += kLoraWarps) {
+      for (int j = 0; j < G; ++j) {
+        if (G > 1 && 8 * j >= w.count) continue;
+#pragma unroll
+        for (int m = 0; m < RT; ++m) {
+          acc[m][j][0] = fadd2(acc[m][j][0], make_float2(part[m][j][0], part[m][j][1]));
+          acc[m][j][1] = fadd2(acc[m][j][1], make_float2(part[m][j][2], part[m][j][3]));
+        }
+      }
+    };
+    auto multiply = [&](auto onto_zero) {
       cp_async_wait<S - 2>();
       // every lane reads only what it copied itself: no other wait.  The slot that is
       // requested now was read by this lane in the step before.
       request();
       const uint4* u4 = reinterpret_cast<const uint4*>(ring + slot * Sm::kUnit) + lane;
       slot = slot + 1 == S ? 0 : slot + 1;
-      // the tensor cores add at most 4 P instructions' products before an FP32 addition
-      float part[RT][G][4];
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) part[m][j][c] = 0.0f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         uint4 xb[G];
@@ -283,24 +289,27 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
 #pragma unroll
           for (int j = 0; j < G; ++j) {
             if (G > 1 && 8 * j >= w.count) continue;
-            mma_bf16(part[m][j], lo.x, hi.x, lo.y, hi.y, xb[j].x, xb[j].y);
+            if (decltype(onto_zero)::value && p == 0) mma_bf16_first(part[m][j], lo.x, hi.x, lo.y, hi.y, xb[j].x, xb[j].y);
+            else mma_bf16(part[m][j], lo.x, hi.x, lo.y, hi.y, xb[j].x, xb[j].y);
             mma_bf16(part[m][j], lo.z, hi.z, lo.w, hi.w, xb[j].z, xb[j].w);
           }
         }
       }
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][j][c] += part[m][j][c];
+    };
+    for (int chunk = w.chunk0 + warp; chunk < w.chunk1; chunk += kLoraWarps) {
+      multiply(LoraTrue{});
+      if (P == 1 && chunk + kLoraWarps < w.chunk1) {
+        chunk += kLoraWarps;
+        multiply(LoraFalse{});
+      }
+      promote();
     }
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int j = 0; j < G; ++j)
         join[(warp * RT * G + m * G + j) * 32 + lane] =
-            make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+            make_float4(acc[m][j][0].x, acc[m][j][0].y, acc[m][j][1].x, acc[m][j][1].y);
     __syncthreads();
     for (int i = threadIdx.x; i < RT * G * 32; i += kLoraThreads) {
       const int m = i / (G * 32), j = i / 32 % G;
