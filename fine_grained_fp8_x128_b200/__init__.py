@@ -487,16 +487,19 @@ def _leading(t):
     units describes it."""
     if t is None:
         return 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("expected a 2D tensor with a contiguous last dimension")
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    return t.stride(0) if shape[0] > 1 else (shape[1] + 15) // 16 * 16
 
 
 def _call(name, tensors, args, stream):
     """Call an entry point on the tensors' device (all of them on one) and its current stream."""
-    given = [t.get_device() for t in tensors if t is not None]
-    device = given[0]
-    if device < 0 or given.count(device) != len(given):
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0:
         raise ValueError(f"{name}: expected CUDA tensors on one device")
     # the raw handle of the device's current stream: a Stream object would cost a third of a small call's host time
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
@@ -509,44 +512,56 @@ def _call(name, tensors, args, stream):
         raise FP8QError(rc, name)
 
 
-def fp8q_layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, q=None, sf=None, stream=None):
-    """Rows of x (BF16 or FP32 [M][N]) normalised, times gamma plus beta ([N], BF16 or FP32, or None): into y
-    (x's type), into the 1x128 tiles q uint8 [M][N] with sf float32 [N/128][ld >= M], or both; optional mean and
-    rstd float32 [M]."""
+def _layer_norm(x, gamma, beta, eps, y, mean, rstd, q, sf, stream):
+    """fp8q_layer_norm with outputs known to fit x."""
     M, N = x.shape
     param = gamma if gamma is not None else beta
     if param is not None:
         _need("gamma", gamma, param.dtype, (N,))
         _need("beta", beta, param.dtype, (N,))
+    _call("fp8q_layer_norm", (x, gamma, beta, y, mean, rstd, q, sf),
+          (_ptr(x), _dtype(x), M, N, _leading(x), _ptr(gamma), _ptr(beta), _dtype(param), eps, _ptr(y), _leading(y),
+           _ptr(mean), _ptr(rstd), _ptr(q), _leading(q), _ptr(sf), _ld(sf) if sf is not None else 0), stream)
+
+
+def fp8q_layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, q=None, sf=None, stream=None):
+    """Rows of x (BF16 or FP32 [M][N]) normalised, times gamma plus beta ([N], BF16 or FP32, or None): into y
+    (x's type), into the 1x128 tiles q uint8 [M][N] with sf float32 [N/128][ld >= M], or both; optional mean and
+    rstd float32 [M]."""
+    M, N = x.shape
     _rows("y", y, x.dtype, x.shape)
     _rows("q", q, torch.uint8, x.shape)
     _need("mean", mean, torch.float32, (M,))
     _need("rstd", rstd, torch.float32, (M,))
     if sf is not None and (sf.dtype != torch.float32 or sf.dim() != 2 or sf.shape[0] != N // 128 or sf.shape[1] < M):
         raise ValueError("sf: expected float32 [N/128][ld >= M]")
-    _call("fp8q_layer_norm", (x, gamma, beta, y, mean, rstd, q, sf),
-          (_ptr(x), _dtype(x), M, N, _leading(x), _ptr(gamma), _ptr(beta), _dtype(param), eps, _ptr(y), _leading(y),
-           _ptr(mean), _ptr(rstd), _ptr(q), _leading(q), _ptr(sf), _ld(sf) if sf is not None else 0), stream)
+    _layer_norm(x, gamma, beta, eps, y, mean, rstd, q, sf, stream)
+
+
+def _layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream):
+    """fp8q_layer_norm_backward with outputs known to fit x."""
+    M, N = x.shape
+    _rows("dy", dy, x.dtype, x.shape)
+    if gamma is not None:
+        _need("gamma", gamma, gamma.dtype, (N,))
+    _need("mean", mean, torch.float32, (M,))
+    _need("rstd", rstd, torch.float32, (M,))
+    _call("fp8q_layer_norm_backward", (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace),
+          (_ptr(dy), _leading(dy), _ptr(x), _leading(x), _dtype(x), M, N, _ptr(gamma), _dtype(gamma), _ptr(mean),
+           _ptr(rstd), _ptr(dx), _leading(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+           workspace.numel() if workspace is not None else 0), stream)
 
 
 def fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None, stream=None):
     """Gradients of fp8q_layer_norm: dx (x's type), dgamma and dbeta float32 [N], each optional.  workspace
     float32, at least fp8q_layer_norm_backward_workspace(M, N) elements, for dgamma and dbeta."""
     M, N = x.shape
-    _rows("dy", dy, x.dtype, x.shape)
     _rows("dx", dx, x.dtype, x.shape)
-    if gamma is not None:
-        _need("gamma", gamma, gamma.dtype, (N,))
-    _need("mean", mean, torch.float32, (M,))
-    _need("rstd", rstd, torch.float32, (M,))
     _need("dgamma", dgamma, torch.float32, (N,))
     _need("dbeta", dbeta, torch.float32, (N,))
     if workspace is not None:
         _need("workspace", workspace, torch.float32, workspace.shape)
-    _call("fp8q_layer_norm_backward", (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace),
-          (_ptr(dy), _leading(dy), _ptr(x), _leading(x), _dtype(x), M, N, _ptr(gamma), _dtype(gamma), _ptr(mean),
-           _ptr(rstd), _ptr(dx), _leading(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
-           workspace.numel() if workspace is not None else 0), stream)
+    _layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream)
 
 
 def fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, workspace,
@@ -669,6 +684,14 @@ def quant_w_128x128(w, transposed: bool = False, stream=None):
     return (q, sf, qt, sft) if transposed else (q, sf)
 
 
+def _under(stream, device):
+    """The given stream as the current one: what is allocated under it is not handed to another stream's work while
+    the stream's kernels may still use it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def _empty_rows(M, N, dtype, device):
     """[M][N] whose rows lie whole 16-byte units apart."""
     per = 16 // dtype.itemsize
@@ -678,54 +701,69 @@ def _empty_rows(M, N, dtype, device):
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """Returns (y of x's type, mean float32 [M], rstd float32 [M])."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return layer_norm(x, gamma, beta, eps)
     M, N = x.shape
     y = _empty_rows(M, N, x.dtype, x.device)
     mean = torch.empty(M, dtype=torch.float32, device=x.device)
     rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    fp8q_layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=stream)
+    _layer_norm(x, gamma, beta, eps, y, mean, rstd, None, None, None)
     return y, mean, rstd
 
 
 def layer_norm_quant(x, gamma=None, beta=None, eps=1e-5, keep_y=False, stream=None):
     """The norm's 1x128 E4M3 tiles: (q uint8 [M][N], sf float32 [N/128][ld], mean, rstd), and y at the end with keep_y."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return layer_norm_quant(x, gamma, beta, eps, keep_y)
     M, N = x.shape
     y = _empty_rows(M, N, x.dtype, x.device) if keep_y else None
     mean = torch.empty(M, dtype=torch.float32, device=x.device)
     rstd = torch.empty(M, dtype=torch.float32, device=x.device)
     q = torch.empty((M, N), dtype=torch.uint8, device=x.device)
     sf = torch.empty((N // 128, sf_ld(M)), dtype=torch.float32, device=x.device)
-    fp8q_layer_norm(x, gamma, beta, eps, y, mean, rstd, q, sf, stream)
+    _layer_norm(x, gamma, beta, eps, y, mean, rstd, q, sf, None)
     return (q, sf, mean, rstd, y) if keep_y else (q, sf, mean, rstd)
 
 
 def layer_norm_backward(dy, x, gamma, mean, rstd, stream=None):
     """Returns (dx of x's type, dgamma float32 [N], dbeta float32 [N])."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return layer_norm_backward(dy, x, gamma, mean, rstd)
     M, N = x.shape
     dx = _empty_rows(M, N, x.dtype, x.device)
     dgamma = torch.empty(N, dtype=torch.float32, device=x.device)
     dbeta = torch.empty(N, dtype=torch.float32, device=x.device)
     ws = torch.empty(max(1, _lib.fp8q_layer_norm_backward_workspace(M, N)), dtype=torch.float32, device=x.device)
-    fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream)
+    _layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, None)
     return dx, dgamma, dbeta
 
 
 def moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down,
                    out_dtype=torch.bfloat16, stream=None):
     """The MoE layer for a few tokens (see fp8q_moe_few_tokens); returns y [T][H]."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, out_dtype)
     T, H = x.shape
     E, I, _ = w_up.shape
     y = torch.empty((T, H), dtype=out_dtype, device=x.device)
     n = _lib.fp8q_moe_few_tokens_workspace(T, expert_ids.shape[1], E, H, I)
     ws = torch.empty(max(1, n), dtype=torch.uint8, device=x.device)
-    fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, ws, stream)
+    fp8q_moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, w_down, sf_down, y, ws)
     return y
 
 
 def lora_apply(x, rows, group_offsets, a, b, scaling, base, out=None, stream=None):
     """base plus each token's adapter (see fp8q_lora_apply), into out (allocated when not given); returns out."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return lora_apply(x, rows, group_offsets, a, b, scaling, base, out)
     if out is None:
         out = _empty_rows(base.shape[0], base.shape[1], base.dtype, base.device)
     n = _lib.fp8q_lora_apply_workspace(x.shape[0], x.shape[1], a.shape[1], group_offsets.shape[0] - 1)
     ws = torch.empty(max(1, n), dtype=torch.float32, device=x.device)
-    fp8q_lora_apply(x, rows, group_offsets, a, b, scaling, base, out, ws, stream)
+    fp8q_lora_apply(x, rows, group_offsets, a, b, scaling, base, out, ws)
     return out

@@ -316,7 +316,7 @@ layer_norm_kernel(const LayerNormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean[r]) * rstd[r], ga[j], be[j]);
         const bool live = row0 + r < a.M;
-        if (a.y != nullptr && live && chk(8 * static_cast<int64_t>(v) + valid - 1, a.ldy, CHK_NORM)) {
+        if (a.y != nullptr && live && valid > 0 && chk(8 * static_cast<int64_t>(v) + valid - 1, a.ldy, CHK_NORM)) {
           Raw8<T> o;
           pack8(o, f);
           store8(static_cast<T*>(a.y) + (row0 + r) * a.ldy + 8 * static_cast<int64_t>(v), o, valid);
@@ -753,7 +753,7 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
             const float xh = (fx[j] - mean[r]) * rstd[r];
             fd[j] = rstd[r] * (fmaf(fd[j], ga[j], -c1[r]) - xh * c2[r]);
           }
-          if (row0 + r < a.M && chk(8 * static_cast<int64_t>(v) + valid - 1, a.lddx, CHK_NORM)) {
+          if (row0 + r < a.M && valid > 0 && chk(8 * static_cast<int64_t>(v) + valid - 1, a.lddx, CHK_NORM)) {
             Raw8<T> o;
             pack8(o, fd);
             store8(static_cast<T*>(a.dx) + (row0 + r) * a.lddx + 8 * static_cast<int64_t>(v), o, valid);
