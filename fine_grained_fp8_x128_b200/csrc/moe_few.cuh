@@ -331,15 +331,15 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
       Item i{0, 0, 0, 0, -1};
       if (item < items) {
         const uint32_t rb = item / blocks, b = item - rb * blocks;
-        i.expert = __ldg(block_expert + b);
-        i.start = __ldg(block_start + b);
-        i.count = __ldg(block_count + b);
+        i.expert = block_expert[b];
+        i.start = block_start[b];
+        i.count = block_count[b];
         i.row = static_cast<int>(rb) * kRows;
       }
       return i;
     };
     auto look_up_column = [&](Item& i) {
-      if (columns && lane < i.count) i.record = MODE == kFewDown ? i.start + lane : __ldg(entry + i.start + lane) / a.k;
+      if (columns && lane < i.count) i.record = MODE == kFewDown ? i.start + lane : entry[i.start + lane] / a.k;
     };
     Item now = look_up(blockIdx.x);
     look_up_column(now);

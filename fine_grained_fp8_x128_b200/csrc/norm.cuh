@@ -44,6 +44,9 @@ struct LayerNormArgs {
 
 // Programmatic dependent launch: let the next launch of the stream begin; wait
 // for the end of the launch before (and so, as every launch waits, of all before).
+// What the launch before wrote is read through plain pointers: a load the compiler
+// may take for one of constant memory (__ldg, const __restrict__) could be moved
+// ahead of the wait.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -961,8 +964,7 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
 // 32 threads a column, then a fixed tree.
 constexpr int kNormJoinThreads = 1024;
 __global__ void __launch_bounds__(kNormJoinThreads)
-layer_norm_bwd_join_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ dgamma,
-                           float* __restrict__ dbeta) {
+layer_norm_bwd_join_kernel(const float* partial, int rows, int N, float* dgamma, float* dbeta) {
   __shared__ float s[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;               // of 2 N columns: dgamma's, then dbeta's
