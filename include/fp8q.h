@@ -21,9 +21,10 @@
  *    Inputs and outputs must not overlap.
  *  - Inputs are finite BF16 values; behaviour for Inf/NaN inputs is unspecified.
  *  - The library allocates no per-call memory.  Its only state is one
- *    device-side status word per device.  One call needs scratch space, and
- *    the caller passes it: fp8q_moe_dispatch_layout takes a workspace sized
- *    by fp8q_moe_dispatch_layout_workspace.
+ *    device-side status word per device.  Calls that need scratch space take
+ *    it from the caller, sized by the function of the call's name with
+ *    _workspace (fp8q_moe_dispatch_layout, fp8q_layer_norm_backward,
+ *    fp8q_moe_few_tokens, fp8q_lora_apply).
  *  - E4M3 is the OCP "E4M3FN" encoding (bias 7, max 448, no infinities).
  *    The cast is round-to-nearest-even with saturation to +-448.
  *  - Tile scale: s = max(fl32(amax / 448), fl32(1e-12)), IEEE FP32 division;
