@@ -757,7 +757,8 @@ def moe_few_tokens(x, expert_ids, expert_weights, w_gate, sf_gate, w_up, sf_up, 
 
 
 def lora_apply(x, rows, group_offsets, a, b, scaling, base, out=None, stream=None):
-    """base plus each token's adapter (see fp8q_lora_apply), into out (allocated when not given); returns out."""
+    """base plus each token's adapter (see fp8q_lora_apply), into out; returns out.  A token in no group keeps its row
+    of out: without an out given, which is then allocated and not cleared, every token has to be in a group."""
     if stream is not None:
         with _under(stream, x.device):
             return lora_apply(x, rows, group_offsets, a, b, scaling, base, out)

@@ -346,8 +346,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
 // words, 64 contiguous bytes a row.  base and B of the coming units are on their
 // way (cp.async into a ring of S units a warp; a lane reads only what it copied)
 // while a unit is multiplied: read when they are needed, 4096 tokens of 8
-// adapters of rank 64 beside 7168 -> 18432 took 108 us.  What is left is issue-bound,
-// so the addresses are kept and advanced.  Places that no copy fills: a column
+// adapters of rank 64 beside 7168 -> 18432 took 108 us, now 80: 49 % of the tensor
+// pipe, half of it for v's second part, and 44 % of the issue slots; so the addresses
+// are kept and advanced.  Places that no copy fills: a column
 // past N or a token that is none holds anything, which stays in that column or
 // row and is not stored; ranks past r multiply zeros of v, so they are zeros
 // from the start.
@@ -537,7 +538,8 @@ __global__ void __launch_bounds__(32 * WARPS) lora_expand_kernel(const LoraArgs 
 // times a.col_units units of 512 columns; a lane owns two neighbouring columns of a unit, whose
 // rows of B (2 r values each) it reads once for all tokens of the block; v is in
 // shared memory in FP32.  64 tokens with an adapter each of rank 16 beside
-// 7168 -> 18432: 21 us on instruction tiles.
+// 7168 -> 18432: 21 us on instruction tiles, now 15, the latency of an item's steps
+// (group, v, B, base).
 // ---------------------------------------------------------------------------
 constexpr int kLoraFewColumns = 2 * kLoraThreads;
 

@@ -219,8 +219,11 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
 // tiles by one chunk of the stage, so that the columns' operands and a stage's
 // bookkeeping serve 4 KB of codes, and the warps' FP32 sums are joined once an
 // item, in chunk order.  (Sixteen warps of one tile each were bound by their
-// instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, where
-// the loads alone take 43.)
+// instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, which
+// now takes 38.6, 6.1 TB/s of codes; the down pass 21.5, 5.4 TB/s.  With 128 tokens
+// over 256 experts the passes take 890 and 450 us at 1965 MHz, bound by the latency
+// of a stage's multiplications; in a row of calls the power limit lowers the clock
+// and they take a quarter longer.)
 // Four more warps keep the ring of S stages full, across items.  One lane issues
 // a copy in some 100 clocks, so the work is spread: three warps issue the TMA
 // boxes of rows x 128 bytes, the fourth one bulk copy a column for its KC records

@@ -359,11 +359,13 @@ layer_norm_kernel(const LayerNormArgs a) {
 // that HBM stays busy while a step's rows are reduced.  gamma, beta and the
 // columns' gradients stay in registers for all rows of the block; the rows are
 // read from the ring twice, for the sums and for the outputs, rather than kept in
-// registers (backward 90 us instead of 94: no spills).  A step's block barrier
-// also tells that the step before is done with its stage.  What bounds these kernels is the issue of instructions, most of them
-// a warp's share of the joins: hence two vectors a thread (one took 66 us for
-// the tiles of 8192 x 7168 BF16; the row kernels, which load a step's rows when
-// it begins, 84.6, and 117 backward).
+// registers, which spilled.  A step's block barrier also tells that the step
+// before is done with its stage.  8192 x 7168 BF16, tiles and backward: 53 and
+// 70 us (and 4.5 for the join), at 34 and 57 % of DRAM: what bounds these kernels
+// is the issue of instructions, at 57 and 53 % of the slots with 14 warps an SM.
+// Rows kept in registers took 57 and 94 us, one vector a thread (twice the warps
+// for the joins) 59 and 93, two rows a step forward 62; the row kernels, which
+// load a step's rows when it begins, 85 and 126.
 // ---------------------------------------------------------------------------
 constexpr int kNormStages = 3;
 constexpr int kNormStreamThreads = 448;                    // up to 144 registers each

@@ -630,7 +630,8 @@ fp8q_status fp8q_gemm_mxf8_ue8m0(const void* a, int64_t lda, const uint32_t* sfa
  * q N % 128 == 0, ldq >= N, ld_sf >= M.  N > 16384 is FP8Q_ERR_UNSUPPORTED.
  * x, y, gamma, beta, q 16-byte aligned, the rows of x and y whole 16-byte
  * units apart (ldx, ldy % 8 == 0 for BF16, % 4 == 0 for FP32), ldq % 16 == 0.
- * N itself may be odd.  M == 0 launches nothing.  One launch.
+ * N itself may be odd.  No output overlaps an input.  M == 0 launches nothing.
+ * One launch.  A row's sums of x and of (x - mu)^2 have to fit FP32.
  */
 fp8q_status fp8q_layer_norm(const void* x, int x_dtype, int64_t M, int64_t N, int64_t ldx, const void* gamma,
                             const void* beta, int param_dtype, float eps, void* y, int64_t ldy, float* mean,
@@ -648,8 +649,8 @@ fp8q_status fp8q_layer_norm(const void* x, int x_dtype, int64_t M, int64_t N, in
  *               elements; needed when dgamma or dbeta is given.  Its contents
  *               need no clearing.  Calls that overlap on the GPU need one each.
  * Every sum has a fixed order: equal inputs give equal bits.
- * Requirements: as fp8q_layer_norm; at least one output.  One launch, and a
- * second for the weight gradients.
+ * Requirements: as fp8q_layer_norm; at least one output, none over an input.
+ * One launch, and a second for the weight gradients.
  */
 int64_t fp8q_layer_norm_backward_workspace(int64_t M, int64_t N);
 fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int x_dtype, int64_t M,
