@@ -258,11 +258,11 @@ fp8q_status launch_lora_expand(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* 
   kern<<<static_cast<unsigned>(grid), kThreads, Sm::kBytes, s>>>(a);
   return launch_status();
 }
-template <typename T, int TOKENS>
+template <typename T>
 fp8q_status lora_expand_few(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev, cudaStream_t s) {
-  constexpr int kPerSm = TOKENS > 2 ? 2 : 4;
-  auto kern = fp8q::lora_expand_few_kernel<T, TOKENS>;
-  int64_t blocks = a.T / TOKENS + (a.groups < a.T ? a.groups : a.T);
+  constexpr int kPerSm = 4;
+  auto kern = fp8q::lora_expand_few_kernel<T>;
+  int64_t blocks = a.T / fp8q::kLoraFewTokens + (a.groups < a.T ? a.groups : a.T);
   if (blocks > a.T) blocks = a.T;
   const int64_t units = ceil_div(a.N, fp8q::kLoraFewColumns);
   a.col_units = lora_col_units(blocks, units, static_cast<int64_t>(kPerSm) * dev->sm_count, 2);
@@ -273,10 +273,13 @@ fp8q_status lora_expand_few(fp8q::LoraArgs a, bool after_shrink, DeviceInfo* dev
   return launch_status();
 }
 template <typename T>
-fp8q_status lora_expand(const fp8q::LoraArgs& a, bool many, DeviceInfo* dev, cudaStream_t s) {
+fp8q_status lora_expand(const fp8q::LoraArgs& a, DeviceInfo* dev, cudaStream_t s) {
   constexpr bool kF32 = sizeof(T) == 4;
   const bool after = a.adapters > 0;
-  if (!many) return a.T <= 2 * a.groups ? lora_expand_few<T, 2>(a, after, dev, s) : lora_expand_few<T, 8>(a, after, dev, s);
+  // Few short rows of B a token: FP32 FMAs.  The whole call beside 7168 -> 18432 BF16 with 64 adapters, FMAs and matrix
+  // instructions (us): 64 tokens of rank 8 19.1, 25.1, rank 16 22.4, 26.3, rank 32 33.0, 31.5; 128 tokens of rank 16 33.4,
+  // 27.9; 300 tokens of 128 adapters of rank 16 67, 47.
+  if (a.r <= fp8q::kLoraFewRank && a.T <= a.groups) return lora_expand_few<T>(a, after, dev, s);
   if (a.r <= 32) return launch_lora_expand<T, 1, 2, 2, 16>(a, after, dev, s);
   if (a.r <= 64) return launch_lora_expand<T, 2, kF32 ? 1 : 2, 2, 16>(a, after, dev, s);
   return launch_lora_expand<T, 4, kF32 ? 1 : 2, 2, 8>(a, after, dev, s);
@@ -477,8 +480,7 @@ fp8q_status fp8q_lora_apply(const void* x, int64_t T, int64_t K, int64_t ldx, co
                             : launch_lora_shrink<4, 1, 2, 2>(g, sh, dev, s);
     if (st != FP8Q_OK) return st;
   }
-  return dtype == FP8Q_OUT_F32 ? lora_expand<float>(g, sh.many, dev, s)
-                               : lora_expand<__nv_bfloat16>(g, sh.many, dev, s);
+  return dtype == FP8Q_OUT_F32 ? lora_expand<float>(g, dev, s) : lora_expand<__nv_bfloat16>(g, dev, s);
 }
 
 }  // extern "C"

@@ -8,13 +8,16 @@
 //   expand   out = base + s_a B_a v
 // With few tokens an adapter the bound is reading A and B once, with many it is
 // x, base and out; the products are 2 r (K + N) a token, far under either.  The
-// shrink and the many-token expansion run on mma.sync with operands loaded
-// straight into fragment order, the few-token expansion on FP32 FMAs (a column a
-// token is r of them, and an instruction tile would be one row in sixteen full).
+// shrink and the expansion run on mma.sync with operands loaded straight into
+// fragment order; for a token an adapter and rows of B of 32 bytes at most the
+// expansion runs on FP32 FMAs (a tile would be one row in sixteen full, and its
+// loads half empty).
 // x, A and B are BF16 as given; as an MMA operand v is split into BF16 parts (two
 // for a BF16 output, which keep v to 2^-16 of itself; three for FP32, 2^-24), so
 // that its rounding stays under the output's.
 #pragma once
+
+#include <type_traits>
 
 #include "moe_few.cuh"
 
@@ -112,6 +115,11 @@ __device__ __forceinline__ int64_t lora_token(const LoraArgs& a, int pos) {
   return t;
 }
 
+// The first `bytes` (at most 128 KB, so that all resident blocks' stay in L2) from p into L2; both multiples of 16.
+__device__ __forceinline__ void bulk_prefetch(const void* p, int64_t bytes) {
+  const uint32_t n = static_cast<uint32_t>(min(bytes, static_cast<int64_t>(128 * 1024)));
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+}
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(live ? 16 : 0) : "memory");
 }
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
 }
 
 // ---------------------------------------------------------------------------
-// Expand, many tokens a group.  An item is a block of up to 16 MB tokens of one group times
+// Expand on matrix instructions.  An item is a block of up to 16 MB tokens of one group times
 // a.col_units units of 32 columns a warp.  Tokens are the rows of the
 // product, v's parts its first operand (in shared memory, fragment order), B's
 // rows the second.  The 8 columns of an instruction stand for columns
@@ -534,22 +542,100 @@ __global__ void __launch_bounds__(32 * WARPS) lora_expand_kernel(const LoraArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Expand, few tokens a group.  An item is a block of up to TOKENS tokens of one group
-// times a.col_units units of 512 columns; a lane owns two neighbouring columns of a unit, whose
-// rows of B (2 r values each) it reads once for all tokens of the block; v is in
-// shared memory in FP32.  64 tokens with an adapter each of rank 16 beside
-// 7168 -> 18432: 21 us on instruction tiles, now 15, the latency of an item's steps
-// (group, v, B, base).
+// Expand, r <= 16 and a token a group on average.  An item is a block of one or two tokens of one
+// group times a.col_units units of 512 columns, 64 a warp.  B's rows are 16 or 32 bytes and lie together,
+// so a warp reads them as they lie, 16 bytes (8 ranks) a lane: a column's one or two
+// lanes share its sum, and 32 or 16 columns make a step.  A lane's ranks are the same in
+// every step, and its part of v stays in registers.  The sums go through shared memory
+// to the lanes that own two neighbouring columns of base and out.  Sums and products are
+// FP32.  An item's part of B and base is on its way to L2 while v is awaited.
+// 64 tokens with an adapter each of rank 16 beside 7168 -> 18432: 14.5 us (a lane with whole
+// rows of B: 16, on matrix instructions 18.5), 2.9 TB/s; what bounds it is the latency of an
+// item's steps (group, token, v, B), which one round of items does not overlap.
 // ---------------------------------------------------------------------------
 constexpr int kLoraFewColumns = 2 * kLoraThreads;
+constexpr int kLoraFewRank = 16, kLoraFewTokens = 2;
+constexpr int kLoraFewSteps = 4;       // loads a lane keeps on their way
 
-template <typename T, int TOKENS>
-__global__ void __launch_bounds__(kLoraThreads, TOKENS > 2 ? 2 : 4) lora_expand_few_kernel(const LoraArgs a) {
+// The item's units for TC tokens; sums: this warp's.
+template <typename T, int TC>
+__device__ __forceinline__ void lora_few_units(const LoraArgs& a, int group, bool adapted, int unit0, int unit1,
+                                               const float (*vs)[kLoraFewRank], const int64_t* tokens,
+                                               float (*sums)[64]) {
+  using Pair = typename std::conditional<sizeof(T) == 4, float2, uint32_t>::type;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool two = a.r > 8;                                       // lanes a column
+  const int columns = two ? 16 : 32, q = two ? lane & 1 : 0, lc = two ? lane >> 1 : lane;
+  float2 v[TC][4];
+#pragma unroll
+  for (int c = 0; c < TC; ++c) {
+    const float4 lo = *reinterpret_cast<const float4*>(&vs[c][8 * q]), hi = *reinterpret_cast<const float4*>(&vs[c][8 * q + 4]);
+    v[c][0] = make_float2(lo.x, lo.y); v[c][1] = make_float2(lo.z, lo.w);
+    v[c][2] = make_float2(hi.x, hi.y); v[c][3] = make_float2(hi.z, hi.w);
+  }
+  for (int u = unit0; u < unit1; ++u) {
+    const int col0 = u * kLoraFewColumns + 64 * warp, col = col0 + 2 * lane;
+    if (col0 >= a.N) break;
+    const bool mine = col < a.N;                                  // N is a multiple of eight
+    Pair base[TC];                                                // on their way while B is multiplied
+#pragma unroll
+    for (int c = 0; c < TC; ++c)
+      if (mine)
+        base[c] = __ldcs(reinterpret_cast<const Pair*>(static_cast<const T*>(a.base) +
+                                                       max(tokens[c], static_cast<int64_t>(0)) * a.ldb + col));
+    if (adapted) {
+      const __nv_bfloat16* rows = a.b + (static_cast<int64_t>(group) * a.N + col0) * a.r + 8 * lane;
+      const int end = min(64, a.N - col0);                        // of the warp's columns
+      for (int c0 = 0; c0 < end; c0 += kLoraFewSteps * columns) {
+        Raw8<__nv_bfloat16> raw[kLoraFewSteps];
+#pragma unroll
+        for (int i = 0; i < kLoraFewSteps; ++i) {
+          const int at = c0 + i * columns;
+          raw[i].w[0] = make_uint4(0, 0, 0, 0);
+          if (at + lc < end) raw[i].w[0] = __ldg(reinterpret_cast<const uint4*>(rows + static_cast<int64_t>(at) * a.r));
+        }
+#pragma unroll
+        for (int i = 0; i < kLoraFewSteps; ++i) {
+          float2 b[4];
+          unpack8(raw[i], b);
+          const int at = c0 + i * columns + lc;
+#pragma unroll
+          for (int c = 0; c < TC; ++c) {
+            float2 p = fmul2(v[c][0], b[0]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) p = ffma2(v[c][j], b[j], p);
+            float sum = p.x + p.y;
+            if (two) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            if (q == 0 && at < end) sums[c][at] = sum;
+          }
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+      const int64_t tok = tokens[c];
+      if (!mine || tok < 0 || !chk(col + 1, a.ldo, CHK_LORA)) continue;
+      const float2 d = adapted ? *reinterpret_cast<const float2*>(&sums[c][2 * lane]) : f2(0.0f);
+      Pair* out = reinterpret_cast<Pair*>(static_cast<T*>(a.out) + tok * a.ldo + col);
+      if constexpr (sizeof(T) == 4) {
+        *out = adapted ? fadd2(base[c], d) : base[c];
+      } else {
+        const float2 o = fadd2(make_float2(bf16lo(base[c]), bf16hi(base[c])), d);
+        *out = adapted ? pack_bf16x2(o.x, o.y) : base[c];
+      }
+    }
+    __syncwarp();                                                 // sums is free again
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_few_kernel(const LoraArgs a) {
   __shared__ LoraGroups gr;
-  __shared__ __align__(16) float vs[TOKENS][kLoraMaxRank];
-  __shared__ int64_t tokens[TOKENS];
-  pdl_wait();
-  const int blocks = lora_groups<kLoraThreads>(gr, a, a.groups, TOKENS);
+  __shared__ __align__(16) float vs[kLoraFewTokens][kLoraFewRank];
+  __shared__ __align__(16) float sums[kLoraWarps][kLoraFewTokens][64];
+  __shared__ int64_t tokens[kLoraFewTokens];
+  const int blocks = lora_groups<kLoraThreads>(gr, a, a.groups, kLoraFewTokens);
   const int units = (a.N + kLoraFewColumns - 1) / kLoraFewColumns;
   const int col_blocks = (units + a.col_units - 1) / a.col_units;
   const int64_t items = static_cast<int64_t>(blocks) * col_blocks;
@@ -557,77 +643,35 @@ __global__ void __launch_bounds__(kLoraThreads, TOKENS > 2 ? 2 : 4) lora_expand_
     const int bl = static_cast<int>(item / col_blocks);
     const int unit0 = static_cast<int>(item % col_blocks) * a.col_units, unit1 = min(unit0 + a.col_units, units);
     const int2 f = lora_find(gr, a.groups, bl);
-    const int first = gr.first[f.x] + f.y * TOKENS;
-    const int count = min(gr.count[f.x] - f.y * TOKENS, TOKENS);
+    const int first = gr.first[f.x] + f.y * kLoraFewTokens;
+    const int count = min(gr.count[f.x] - f.y * kLoraFewTokens, kLoraFewTokens);
     const bool adapted = f.x < a.adapters;
     if (!adapted && a.base == a.out) continue;                   // nothing to add, nowhere to copy
+    const int64_t col0 = static_cast<int64_t>(unit0) * kLoraFewColumns;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(unit1) * kLoraFewColumns, static_cast<int64_t>(a.N)) - col0);
+    if (threadIdx.x == 32 && adapted)
+      bulk_prefetch(a.b + (static_cast<int64_t>(f.x) * a.N + col0) * a.r, static_cast<int64_t>(cols) * a.r * 2);
     __syncthreads();                                             // the item before is done with vs
-    if (static_cast<int>(threadIdx.x) < count) tokens[threadIdx.x] = lora_token(a, first + threadIdx.x);
+    if (static_cast<int>(threadIdx.x) < count) {
+      const int64_t tok = lora_token(a, first + threadIdx.x);
+      tokens[threadIdx.x] = tok;
+      if (tok >= 0) bulk_prefetch(static_cast<const T*>(a.base) + tok * a.ldb + col0, static_cast<int64_t>(cols) * sizeof(T));
+    }
+    pdl_wait();
     const float scale = adapted && a.scaling != nullptr ? __ldg(a.scaling + f.x) : 1.0f;
-    const int n = adapted ? count * a.r : 0;
-    for (int i = threadIdx.x; i < n; i += kLoraThreads) {
-      const int c = i / a.r, rank = i - c * a.r;
+    if (adapted && static_cast<int>(threadIdx.x) < count * a.r) {
+      const int c = threadIdx.x / a.r, rank = threadIdx.x - c * a.r;
       const float* src = a.v + static_cast<int64_t>(first + c) * a.r + rank;
       float s = 0.0f;
-      for (int u = 0; u < a.slices; ++u, src += a.T * a.r) s += *src;
+#pragma unroll 4
+      for (int u = 0; u < a.slices; ++u) s += src[u * a.T * a.r];
       vs[c][rank] = s * scale;
     }
     __syncthreads();
-    for (int u = unit0; u < unit1; ++u) {
-      const int col = u * kLoraFewColumns + 2 * threadIdx.x;
-      if (col >= a.N) break;                                     // N is a multiple of eight
-      float2 base[TOKENS];                               // on their way while B is multiplied
-#pragma unroll
-      for (int c = 0; c < TOKENS; ++c) {
-        if (c >= count) break;
-        const int64_t o = max(tokens[c], static_cast<int64_t>(0)) * a.ldb + col;
-        if (sizeof(T) == 4) {
-          base[c] = __ldcs(reinterpret_cast<const float2*>(static_cast<const float*>(a.base) + o));
-        } else {
-          const uint32_t w = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.base) + o));
-          base[c] = make_float2(bf16lo(w), bf16hi(w));
-        }
-      }
-      float2 acc[TOKENS][2];                             // a token's two columns, even and odd ranks apart
-#pragma unroll
-      for (int c = 0; c < TOKENS; ++c) acc[c][0] = acc[c][1] = f2(0.0f);
-      if (adapted) {
-        const __nv_bfloat16* rows = a.b + (static_cast<int64_t>(f.x) * a.N + col) * a.r;
-#pragma unroll 2
-        for (int rank = 0; rank < a.r; rank += 8) {
-          Raw8<__nv_bfloat16> raw[2];
-          float2 b[2][4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            raw[k].w[0] = __ldg(reinterpret_cast<const uint4*>(rows + k * a.r + rank));
-            unpack8(raw[k], b[k]);
-          }
-#pragma unroll
-          for (int c = 0; c < TOKENS; ++c) {
-            if (c >= count) break;
-            const float4 p = *reinterpret_cast<const float4*>(&vs[c][rank]), q = *reinterpret_cast<const float4*>(&vs[c][rank + 4]);
-            const float2 v[4] = {make_float2(p.x, p.y), make_float2(p.z, p.w), make_float2(q.x, q.y), make_float2(q.z, q.w)};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[c][k] = ffma2(v[j], b[k][j], acc[c][k]);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < TOKENS; ++c) {
-        if (c >= count) break;
-        const int64_t tok = tokens[c];
-        if (tok < 0 || !chk(col + 1, a.ldo, CHK_LORA)) continue;
-        const float2 o = adapted ? fadd2(base[c], make_float2(acc[c][0].x + acc[c][0].y, acc[c][1].x + acc[c][1].y))
-                                 : base[c];
-        if (sizeof(T) == 4)
-          *reinterpret_cast<float2*>(static_cast<float*>(a.out) + tok * a.ldo + col) = o;
-        else
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.ldo + col) = pack_bf16x2(o.x, o.y);
-      }
-    }
+    if (count == 1) lora_few_units<T, 1>(a, f.x, adapted, unit0, unit1, vs, tokens, sums[threadIdx.x >> 5]);
+    else lora_few_units<T, 2>(a, f.x, adapted, unit0, unit1, vs, tokens, sums[threadIdx.x >> 5]);
   }
+  pdl_wait();                                                    // of a block without an item, too
 }
 
 }  // namespace fp8q

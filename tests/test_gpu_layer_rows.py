@@ -73,8 +73,8 @@ def test_moe(fp8q, T, k, E, gated):
     assert fp8q.fp8q_device_status() == 0
 
 
-# few tokens a group in blocks of 2 and of 8, and many
-@pytest.mark.parametrize("T,n,r", [(6, 4, 16), (30, 4, 24), (300, 4, 8), (300, 3, 40), (300, 2, 128)])
+# a token a group with short rows of B, few tokens a group, and many
+@pytest.mark.parametrize("T,n,r", [(7, 7, 16), (6, 4, 16), (30, 4, 24), (300, 4, 8), (300, 3, 40), (300, 2, 128)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_lora(fp8q, T, n, r, dtype):
     x, a, b, scaling, base, ids = make(T, n, r, 520, 264, dtype, seed=T + r)
