@@ -149,7 +149,7 @@ fp8q_status launch_norm_bwd(const fp8q::LayerNormBwdArgs& a, const NormShape& sh
 template <int MODE, int RT, int S>
 fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  using Sm = fp8q::FewSmem<RT, S>;
+  using Sm = fp8q::FewSmem<MODE, RT, S>;
   auto kern = fp8q::few_weights_kernel<MODE, RT, S>;
   fp8q_status st = allow_smem(kern, Sm::kBytes, &done[dev - g_dev]);
   if (st != FP8Q_OK) return st;
@@ -162,7 +162,8 @@ fp8q_status launch_few_weights(const fp8q::FewArgs& a, DeviceInfo* dev, cudaStre
   return launch_after(kern, dim3(dev->sm_count), fp8q::kFewWeightThreads, Sm::kBytes, s, map_lo, map_hi, a);
 }
 
-template <int RT, int S>
+// Row tiles an item and stages of the up pass (RT, S) and of the down pass (RTD, SD).
+template <int RT, int S, int RTD, int SD>
 fp8q_status moe_few(const fp8q::FewArgs& a, int y_dtype, DeviceInfo* dev, cudaStream_t s) {
   fp8q_status st;
   fp8q::few_plan_kernel<<<static_cast<unsigned>(1 + ceil_div(static_cast<int64_t>(a.T) * (a.H / 128), 32)), 1024, 0,
@@ -175,7 +176,7 @@ fp8q_status moe_few(const fp8q::FewArgs& a, int y_dtype, DeviceInfo* dev, cudaSt
   const int64_t grid = grid_for(ceil_div(chunks, fp8q::kFewThreads / 32), dev->sm_count, 8);
   st = launch_after(fp8q::few_hidden_kernel, dim3(static_cast<unsigned>(grid)), fp8q::kFewThreads, 0, s, a);
   if (st != FP8Q_OK) return st;
-  if ((st = launch_few_weights<fp8q::kFewDown, RT, S>(a, dev, s)) != FP8Q_OK) return st;
+  if ((st = launch_few_weights<fp8q::kFewDown, RTD, SD>(a, dev, s)) != FP8Q_OK) return st;
   const dim3 cg(static_cast<unsigned>(ceil_div(a.H, 512)), static_cast<unsigned>(a.T));
   return y_dtype == FP8Q_OUT_F32 ? launch_after(fp8q::few_combine_kernel<float>, cg, 64, 0, s, a)
                                  : launch_after(fp8q::few_combine_kernel<__nv_bfloat16>, cg, 64, 0, s, a);
@@ -422,10 +423,12 @@ fp8q_status fp8q_moe_few_tokens(const void* x, int64_t T, int64_t H, int64_t ldx
   a.l = fp8q::few_layout(T, k, E, H, I);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Row tiles an item: few entries need small items to fill the SMs evenly, many are better off with fewer, larger
-  // boxes.  7168 -> 2048 -> 7168, top-8, the whole call with 2, 4 and 8 tiles (us): 1 token 69, 75, 75; 4 tokens 145,
-  // 147, 148; 16 tokens (64 experts, no gate) 215, 214, 220; 128 tokens 1480, 1405, 1367.
-  if (T * k <= 64) return moe_few<2, 4>(a, y_dtype, dev, s);
-  return T * k <= 512 ? moe_few<4, 5>(a, y_dtype, dev, s) : moe_few<8, 5>(a, y_dtype, dev, s);
+  // boxes; the down pass, with two parts a column, has room for four stages only from 4 tiles on.  7168 -> 2048 -> 7168,
+  // top-8, the call's device time with 2, 4 and 8 tiles (us, a few calls at 1965 MHz): 1 token 72.6, 76.1, 76.8; 4 tokens
+  // 201, 204, 212; 16 tokens (64 experts, no gate) 219, 220, 226; 128 tokens 1506, 1429, 1429.  2 tiles and three stages
+  // in the down pass too: 1 token 74.6, 16 tokens 234.
+  if (T * k <= 64) return moe_few<2, 4, 4, 4>(a, y_dtype, dev, s);
+  return T * k <= 512 ? moe_few<4, 5, 4, 4>(a, y_dtype, dev, s) : moe_few<8, 5, 8, 5>(a, y_dtype, dev, s);
 }
 
 int64_t fp8q_lora_apply_workspace(int64_t T, int64_t K, int64_t r, int64_t groups) {

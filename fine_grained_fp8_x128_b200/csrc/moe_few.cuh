@@ -7,9 +7,10 @@
 // With a handful of tokens an expert every weight byte is used once or a few
 // times, so the layer is bound by reading the picked experts' codes once.  The
 // activations are NOT quantized: they go to the tensor cores as FP16 with an
-// exact power-of-two scale per 128-wide chunk, the codes are widened E4M3 ->
-// FP16 in registers (exact), products are summed in FP32 over one 128-wide
-// chunk and then multiplied by the weight block's and the chunk's scales.
+// exact power-of-two scale per 128-wide chunk (a hidden row as two FP16 parts,
+// which keep it to 2^-22), the codes are widened E4M3 -> FP16 in registers
+// (exact), products are summed in FP32 over one 128-wide chunk and then
+// multiplied by the weight block's and the chunk's scales.
 // mma.sync rather than tcgen05: the widened codes would have to go back through
 // shared memory to be a tcgen05 operand, twice the bytes that came in, and at
 // these token counts the matrix instructions are far from their limit.
@@ -39,7 +40,8 @@ constexpr int kFewWarps = 8;                  // of a weight pass, which multipl
 constexpr int kFewLoaders = 4;                // and of those that load
 constexpr int kFewWeightThreads = 32 * (kFewWarps + kFewLoaders);
 constexpr int kFewTiles = 2;                  // row tiles a multiplying warp takes
-constexpr int kFewRecord = 272;               // a chunk's 128 FP16 values and its scale, 16-byte units
+// a chunk's record: 128 FP16 values, as many lower parts in a hidden row's, and the scale, in 16-byte units
+constexpr int kFewRecord = 272, kFewHiddenRecord = 528;
 
 // What the plan leaves for the other launches.  Positions number the entries
 // (token, slot) expert by expert, each expert's first position a multiple of 8.
@@ -77,7 +79,7 @@ __host__ __device__ inline FewLayout few_layout(int64_t T, int64_t k, int64_t E,
   l.entry = o; o = few_align(o + 4 * l.max_positions);
   l.xr = o; o = few_align(o + kFewRecord * T * (H / 128));
   l.hid = o; o = few_align(o + 4 * l.max_positions * I);
-  l.hr = o; o = few_align(o + kFewRecord * l.max_positions * (I / 128));
+  l.hr = o; o = few_align(o + kFewHiddenRecord * l.max_positions * (I / 128));
   l.yp = o; o = few_align(o + 4 * n * H);
   l.bytes = o;
   return l;
@@ -106,14 +108,16 @@ __device__ __forceinline__ T* few_at(const FewArgs& a, int64_t off) { return rei
 // magnitude into [2^14, 2^15), and the inverse power.  The scaling is exact, FP16
 // keeps 11 bits (a BF16 value has 8, so x is exact) down to 2^-28 of the
 // chunk's maximum, and what lies below is off by at most 2^-40 of that maximum,
-// under the FP32 accumulation's own rounding.  A hidden value is off by at most
-// 2^-11 of itself.  The power is at most 2^84, so that its inverse times a block
+// under the FP32 accumulation's own rounding.  A hidden value is two of them,
+// the nearest and what is left (kTwo), and off by at most 2^-22 of itself or
+// 2^-40 of the maximum.  The power is at most 2^84, so that its inverse times a block
 // scale (>= 1e-12) is a normal FP32 number: a chunk under 2^-98 loses bits,
 // 2^-109 at most.
 // Value k = 32 t + 8 q + i lies at 16-byte unit 4 q + t, place i: the order in
 // which lanes t of a warp read their multiplier operand, without bank conflicts.
 // A warp owns one chunk, four consecutive values a lane.
 // ---------------------------------------------------------------------------
+template <bool kTwo>
 __device__ __forceinline__ void few_record(const float (&f)[4], uint8_t* dst, int lane) {
   float m = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 #pragma unroll
@@ -121,13 +125,21 @@ __device__ __forceinline__ void few_record(const float (&f)[4], uint8_t* dst, in
   int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;   // m >= 0: no sign bit
   e = max(e, -70);
   const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-  const __half2 h0 = __floats2half2_rn(f[0] * up, f[1] * up), h1 = __floats2half2_rn(f[2] * up, f[3] * up);
-  uint2 o;
-  o.x = *reinterpret_cast<const uint32_t*>(&h0);
-  o.y = *reinterpret_cast<const uint32_t*>(&h1);
+  float v[4] = {f[0] * up, f[1] * up, f[2] * up, f[3] * up};
   const int t = lane >> 3, q = (lane & 7) >> 1;
-  *reinterpret_cast<uint2*>(dst + (4 * q + t) * 16 + 8 * (lane & 1)) = o;
-  if (lane == 0) *reinterpret_cast<float*>(dst + 256) = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+  uint8_t* at = dst + (4 * q + t) * 16 + 8 * (lane & 1);
+#pragma unroll
+  for (int part = 0; part < (kTwo ? 2 : 1); ++part) {
+    const __half2 h0 = __floats2half2_rn(v[0], v[1]), h1 = __floats2half2_rn(v[2], v[3]);
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t*>(&h0);
+    o.y = *reinterpret_cast<const uint32_t*>(&h1);
+    *reinterpret_cast<uint2*>(at + 256 * part) = o;
+    const float d[4] = {__low2float(h0), __high2float(h0), __low2float(h1), __high2float(h1)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = isinf(d[i]) ? 0.0f : v[i] - d[i];
+  }
+  if (lane == 0) *reinterpret_cast<float*>(dst + (kTwo ? 512 : 256)) = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 }
 
 // Inclusive scan of two counters over 1024 threads.
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
     const int t = item / chunks, kb = item - t * chunks;
     const uint2 r = *reinterpret_cast<const uint2*>(a.x + t * a.ldx + kb * 128 + 4 * lane);
     const float f[4] = {bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y)};
-    few_record(f, few_at<uint8_t>(a, a.l.xr) + static_cast<int64_t>(item) * kFewRecord, lane);
+    few_record<false>(f, few_at<uint8_t>(a, a.l.xr) + static_cast<int64_t>(item) * kFewRecord, lane);
     return;
   }
   __shared__ int count[kFewMaxExperts], start[kFewMaxExperts];
@@ -220,10 +232,15 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
 // bookkeeping serve 4 KB of codes, and the warps' FP32 sums are joined once an
 // item, in chunk order.  (Sixteen warps of one tile each were bound by their
 // instructions: 59 us for one token's up pass, 8 experts of 7168 -> 2048, which
-// now takes 38.6, 6.1 TB/s of codes; the down pass 21.5, 5.4 TB/s.  With 128 tokens
-// over 256 experts the passes take 890 and 450 us at 1965 MHz, bound by the latency
+// now takes 38.6, 6.1 TB/s of codes; the down pass 23.7, 4.9 TB/s.  With 128 tokens
+// over 256 experts the passes take 876 and 536 us at 1965 MHz, bound by the latency
 // of a stage's multiplications; in a row of calls the power limit lowers the clock
 // and they take a quarter longer.)
+// The down pass multiplies both parts of a hidden row: with one FP16 number a row it
+// took 21.5 and 443 us, and every result, the FP32 ones too, was off by some 2^-12.
+// Lower parts in the columns that a block of four or fewer leaves spare gained
+// nothing: a loop for each form 71.7 us against 72.5 for the one-token call, a
+// branch within the loop 76.7.
 // Four more warps keep the ring of S stages full, across items.  One lane issues
 // a copy in some 100 clocks, so the work is spread: three warps issue the TMA
 // boxes of rows x 128 bytes, the fourth one bulk copy a column for its KC records
@@ -265,18 +282,19 @@ __device__ __forceinline__ void few_join_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
 }
 
-template <int RT, int S>
+template <int MODE, int RT, int S>
 struct FewSmem {
+  static constexpr int kRecord = MODE == kFewDown ? kFewHiddenRecord : kFewRecord;
   static constexpr int kKC = kFewWarps * kFewTiles / RT;
   static constexpr int kChunkBytes = RT * 16 * 128;                      // a chunk's codes
   // a column's records, an odd number of 64-byte halves apart: neighbouring columns use the other half of the banks
-  static constexpr int kColumn = (kKC * kFewRecord) % 128 == 64 ? kKC * kFewRecord : kKC * kFewRecord / 128 * 128 + 64 + (kKC * kFewRecord % 128 > 64 ? 128 : 0);
+  static constexpr int kColumn = (kKC * kRecord + 63) / 128 * 128 + 64;
   static constexpr int kScales = kKC * kChunkBytes + 8 * kColumn;    // 2 KC block scales
   static constexpr int kStage = (kScales + 8 * kKC + 1023) / 1024 * 1024;
   static constexpr int kRing = S * kStage;
   static constexpr int kJoin = kFewWarps * kFewTiles * 512;
   static constexpr int kBytes = 1024 + kRing + kJoin + 32 * S + 16;      // 1024: the ring's alignment
-  static_assert(kColumn >= kKC * kFewRecord && kColumn % 128 == 64, "column stride");
+  static_assert(kColumn >= kKC * kRecord && kColumn % 128 == 64, "column stride");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -284,8 +302,9 @@ template <int MODE, int RT, int S>
 __global__ void __launch_bounds__(kFewWeightThreads)
 few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_constant__ CUtensorMap map_hi,
                    const FewArgs a) {
-  using Sm = FewSmem<RT, S>;
+  using Sm = FewSmem<MODE, RT, S>;
   constexpr int KC = Sm::kKC;
+  constexpr int kRecord = Sm::kRecord, kParts = MODE == kFewDown ? 2 : 1;
   constexpr int kRows = MODE == kFewGated ? 8 * RT : 16 * RT;            // output rows an item, and a box's
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -354,21 +373,21 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
       const Item after = look_up(item + 2 * gridDim.x);
       const int row0 = now.expert * N + now.row;
       const float* scale = scales + static_cast<int64_t>(row0 / 128) * KB + sc;
-      const uint8_t* col = records + static_cast<int64_t>(max(now.record, 0)) * KB * kFewRecord;
+      const uint8_t* col = records + static_cast<int64_t>(max(now.record, 0)) * KB * kRecord;
       for (int c0 = 0; c0 < KB; c0 += KC) {
         if (!warp_wait_converged(&empty[slot], phase, abort_flag, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
         const int n = min(KC, KB - c0);
         uint8_t* stage = ring + slot * Sm::kStage;
         if (columns) {
           if (now.record >= 0)
-            bulk_load(stage + KC * Sm::kChunkBytes + lane * Sm::kColumn, col + c0 * kFewRecord, n * kFewRecord,
+            bulk_load(stage + KC * Sm::kChunkBytes + lane * Sm::kColumn, col + c0 * kRecord, n * kRecord,
                       &full[slot]);
           if (lane < kBoxes && sc < n) cp_async4(stage + Sm::kScales + 4 * lane, scale + c0);
           cp_async_arrive(&full[slot]);
         } else if (lane == 0) {
           if (loader == 0) {
             stage_item[slot] = make_int4(now.count, now.start, now.row, 0);
-            mbar_arrive_expect_tx(&full[slot], n * (Sm::kChunkBytes + now.count * kFewRecord));
+            mbar_arrive_expect_tx(&full[slot], n * (Sm::kChunkBytes + now.count * kRecord));
           }
 #pragma unroll
           for (int i = 0; i < (kBoxes + kBoxLoaders - 1) / kBoxLoaders; ++i) {
@@ -401,7 +420,7 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
   const int code_lo = kc * Sm::kChunkBytes + (MODE == kFewGated ? 8 * rt0 + g : 16 * rt0 + g) * 128;
   const int code_hi = code_lo + (MODE == kFewGated ? 8 * RT : 8) * 128;
   const int sw0 = ((2 * t) ^ g) * 16, sw1 = ((2 * t + 1) ^ g) * 16;
-  const int col_at = KC * Sm::kChunkBytes + kc * kFewRecord;
+  const int col_at = KC * Sm::kChunkBytes + kc * kRecord;
   uint32_t slot = 0, phase = 0;
   for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
     float acc[TW][4];
@@ -423,11 +442,13 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
         const uint8_t* stage = ring + slot * Sm::kStage;
         const float* block_scale = reinterpret_cast<const float*>(stage + Sm::kScales) + kc;
         const float w0 = block_scale[0], w1 = MODE == kFewGated ? block_scale[KC] : w0;
-        float part[TW][4];
+        float part[kParts][TW][4];            // a hidden row's parts have sums of their own: neither waits for the other
 #pragma unroll
-        for (int m = 0; m < TW; ++m)
+        for (int p = 0; p < kParts; ++p)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) part[m][c] = 0.0f;
+          for (int m = 0; m < TW; ++m)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part[p][m][c] = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t l4[TW][4], h4[TW][4];
@@ -448,21 +469,32 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
               widen4(h4[m][2 * q], ah[m][0], ah[m][1]);
               widen4(h4[m][2 * q + 1], ah[m][2], ah[m][3]);
             }
-            const uint4 c = *reinterpret_cast<const uint4*>(stage + col_at + g * Sm::kColumn + (4 * (2 * h + q) + t) * 16);
+            uint4 c[kParts];
 #pragma unroll
-            for (int m = 0; m < TW; ++m) mma_f16(part[m], al[m][0], ah[m][0], al[m][1], ah[m][1], c.x, c.y);
+            for (int p = 0; p < kParts; ++p)
+              c[p] = *reinterpret_cast<const uint4*>(stage + col_at + g * Sm::kColumn + 256 * p + (4 * (2 * h + q) + t) * 16);
 #pragma unroll
-            for (int m = 0; m < TW; ++m) mma_f16(part[m], al[m][2], ah[m][2], al[m][3], ah[m][3], c.z, c.w);
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int m = 0; m < TW; ++m) mma_f16(part[p][m], al[m][0], ah[m][0], al[m][1], ah[m][1], c[p].x, c[p].y);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int m = 0; m < TW; ++m) mma_f16(part[p][m], al[m][2], ah[m][2], al[m][3], ah[m][3], c[p].z, c[p].w);
           }
         }
-        const uint8_t* sc = stage + col_at + 2 * t * Sm::kColumn + 256;
+        const uint8_t* sc = stage + col_at + 2 * t * Sm::kColumn + 256 * kParts;
         const float c0 = *reinterpret_cast<const float*>(sc), c1 = *reinterpret_cast<const float*>(sc + Sm::kColumn);
 #pragma unroll
         for (int m = 0; m < TW; ++m) {
-          acc[m][0] = fmaf(part[m][0], w0 * c0, acc[m][0]);
-          acc[m][1] = fmaf(part[m][1], w0 * c1, acc[m][1]);
-          acc[m][2] = fmaf(part[m][2], w1 * c0, acc[m][2]);
-          acc[m][3] = fmaf(part[m][3], w1 * c1, acc[m][3]);
+          if constexpr (kParts == 2) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part[0][m][c] += part[1][m][c];
+          }
+          acc[m][0] = fmaf(part[0][m][0], w0 * c0, acc[m][0]);
+          acc[m][1] = fmaf(part[0][m][1], w0 * c1, acc[m][1]);
+          acc[m][2] = fmaf(part[0][m][2], w1 * c0, acc[m][2]);
+          acc[m][3] = fmaf(part[0][m][3], w1 * c1, acc[m][3]);
         }
       }
       __syncwarp();
@@ -523,7 +555,7 @@ __global__ void __launch_bounds__(kFewThreads) few_hidden_kernel(const FewArgs a
     const float4 v = *reinterpret_cast<const float4*>(few_at<const float>(a, a.l.hid) + static_cast<int64_t>(item) * 128 +
                                                       4 * lane);
     const float f[4] = {v.x, v.y, v.z, v.w};
-    few_record(f, few_at<uint8_t>(a, a.l.hr) + static_cast<int64_t>(item) * kFewRecord, lane);
+    few_record<true>(f, few_at<uint8_t>(a, a.l.hr) + static_cast<int64_t>(item) * kFewHiddenRecord, lane);
   }
 }
 

@@ -667,9 +667,9 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
  *   h = silu(Wg[e] x[t]) * (Wu[e] x[t]),  silu(v) = v / (1 + exp(-v))
  *   without a gate matrix: h = Wu[e] x[t]
  * W[n,k] = decode(code) * its block's scale.  x is taken as it is (BF16, not
- * quantized) and hidden values as FP16 with a power-of-two scale per 128
- * (off by at most 2^-11 of the value, or 2^-109 where that is more); products
- * and sums are FP32.
+ * quantized) and hidden values as two FP16 parts with a power-of-two scale per
+ * 128 (off by at most 2^-22 of the value, 2^-40 of the largest of its 128, or
+ * 2^-109, whichever is most); products and sums are FP32.
  *   x              : BF16 [T][ldx], H wide.
  *   expert_ids     : device int32 [T][k].  A negative id skips the entry (an
  *                    expert that lives elsewhere); one >= E skips it and records
