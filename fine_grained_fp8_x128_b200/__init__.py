@@ -554,7 +554,7 @@ def _layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
 
 def fp8q_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None, stream=None):
     """Gradients of fp8q_layer_norm: dx (x's type), dgamma and dbeta float32 [N], each optional.  workspace
-    float32, at least fp8q_layer_norm_backward_workspace(M, N) elements, for dgamma and dbeta."""
+    float32, at least fp8q_layer_norm_backward_workspace(M, N) elements, 16-byte aligned, for dgamma and dbeta."""
     M, N = x.shape
     _rows("dx", dx, x.dtype, x.shape)
     _need("dgamma", dgamma, torch.float32, (N,))

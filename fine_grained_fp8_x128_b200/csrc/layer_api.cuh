@@ -350,7 +350,7 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
   const int64_t per16 = 16 / elem_size(x_dtype);
   if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return FP8Q_ERR_ALIGNMENT;
   if (M > 0 && (!aligned(dy, 16) || !aligned(x, 16) || lddy % per16 != 0 || ldx % per16 != 0 || !aligned(gamma, 16) ||
-                !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 4) ||
+                !aligned(mean, 4) || !aligned(rstd, 4) || (grads && !aligned(workspace, 16)) ||
                 (dx != nullptr && (!aligned(dx, 16) || lddx % per16 != 0))))
     return FP8Q_ERR_ALIGNMENT;
   DeviceInfo* dev = nullptr;

@@ -646,8 +646,8 @@ fp8q_status fp8q_layer_norm(const void* x, int x_dtype, int64_t M, int64_t N, in
  *   dx        : optional [M][lddx] of x_dtype.
  *   dgamma, dbeta : optional FP32 [N], written whole (zeros for M == 0).
  *   workspace : FP32, at least fp8q_layer_norm_backward_workspace(M, N)
- *               elements; needed when dgamma or dbeta is given.  Its contents
- *               need no clearing.  Calls that overlap on the GPU need one each.
+ *               elements, 16-byte aligned; needed when dgamma or dbeta is
+ *               given, else not used.  Its contents need no clearing.  Calls that overlap on the GPU need one each.
  * Every sum has a fixed order: equal inputs give equal bits.
  * Requirements: as fp8q_layer_norm; at least one output, none over an input.
  * One launch, and a second for the weight gradients.
