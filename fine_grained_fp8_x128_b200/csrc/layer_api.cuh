@@ -69,13 +69,25 @@ bool norm_streams(int64_t M, int64_t N, int rows, int64_t bytes) {
          fp8q::kNormStages * rows * N * bytes <= 192 * 1024;
 }
 int norm_stream_threads(int64_t N) { return static_cast<int>(ceil_div(N / 8, 64) * 32); }
-// Blocks an SM: as many as their registers allow.
-int norm_stream_blocks(int64_t N) { return fp8q::kNormStreamThreads / norm_stream_threads(N); }
+// Blocks an SM of steps of `rows` rows of `bytes` a column: as many as their registers and their shared memory (the ring,
+// and 3 KB a block: the joins' parts and what the system keeps) allow.
+int norm_stream_blocks(int64_t N, int rows, int64_t bytes) {
+  const int64_t regs = fp8q::kNormStreamThreads / norm_stream_threads(N);
+  const int64_t smem = 228 * 1024 / (fp8q::kNormStages * rows * N * bytes + 3 * 1024);
+  return static_cast<int>(regs < smem ? regs : smem);
+}
 
 // Blocks of the backward pass, and so partial rows: a function of the sizes
-// alone, so that the same call always adds in the same order.
+// alone, so that the same call always adds in the same order.  A block of the
+// streams takes as many steps as its ring has stages at least (that is 198 blocks or more):
+// 1184 x 520 BF16 8.0 us with 198 blocks, 10.8 with the 1036 that fit at once; FP32 8192 x 2048
+// 39.6 us with the two blocks an SM that fit, 49.3 with three.
 int64_t norm_bwd_blocks(int64_t M, int64_t N, int64_t elem) {
-  if (norm_streams(M, N, fp8q::kNormBwdRows, 2 * elem)) return 148 * norm_stream_blocks(N);
+  if (norm_streams(M, N, fp8q::kNormBwdRows, 2 * elem)) {
+    const int64_t few = ceil_div(ceil_div(M, fp8q::kNormBwdRows), fp8q::kNormStages);
+    const int64_t most = 148 * norm_stream_blocks(N, fp8q::kNormBwdRows, 2 * elem);
+    return few < most ? few : most;
+  }
   const NormShape s = norm_shape(N, kNormBwdOneVec);
   const int64_t rows = s.warp_row ? 2 * (fp8q::kNormWarpRowThreads / 32) : 2;
   const int64_t cap = 148 * (s.threads > 512 ? 1 : (s.threads > 256 ? 2 : 4));
@@ -108,7 +120,7 @@ fp8q_status launch_norm_stream(const fp8q::LayerNormArgs& a, DeviceInfo* dev, cu
   auto kern = fp8q::layer_norm_stream_kernel<T, W, R, kTiles>;
   fp8q_status st = allow_smem(kern, kMost, &done[dev - g_dev]);
   if (st != FP8Q_OK) return st;
-  const int64_t grid = grid_for(ceil_div(a.M, R), dev->sm_count, norm_stream_blocks(a.N));
+  const int64_t grid = grid_for(ceil_div(a.M, R), dev->sm_count, norm_stream_blocks(a.N, R, sizeof(T)));
   kern<<<static_cast<unsigned>(grid), norm_stream_threads(a.N),
          static_cast<size_t>(fp8q::kNormStages) * R * a.N * sizeof(T), s>>>(a);
   return launch_status();

@@ -1,5 +1,5 @@
 """The workspaces of the operators around a projection, on the host: a start that the kernels' vector accesses cannot use
-is refused."""
+is refused; and the norm's partial rows are no more than its steps need."""
 import pytest
 
 from common import load_fp8q
@@ -30,3 +30,11 @@ def test_norm_backward_workspace_alignment(fp8q, M, N, dtype):
     if not fp8q.torch.cuda.is_available():
         assert call(FAKE, FAKE, FAKE) == fp8q.FP8Q_ERR_CUDA
         assert call(FAKE + 4, None, None) == fp8q.FP8Q_ERR_CUDA          # no weight gradients: it is not used
+
+
+@pytest.mark.parametrize("M", [1184, 1185, 2368, 5000, 8192])
+@pytest.mark.parametrize("N", [520, 1024, 1536, 2048, 3584])
+def test_partial_rows_of_the_streams(fp8q, M, N):
+    """A block of the streams, and so a partial row, has at least as many steps of two rows as its ring has stages."""
+    rows = fp8q.lib().fp8q_layer_norm_backward_workspace(M, N) // (2 * N)
+    assert rows <= ((M + 1) // 2 + 2) // 3
