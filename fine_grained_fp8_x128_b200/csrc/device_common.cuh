@@ -56,8 +56,8 @@ enum : uint32_t {
   CHK_GEMM_SFD = 23,  // GEMM FP8 epilogue scales
   CHK_GROUP = 24,     // grouped GEMM: a tile's rows inside its group and M_total
   CHK_LAYOUT = 25,    // dispatch layout and regroup: row maps
-  CHK_NORM = 26,      // layer norm: rows, statistics, gradients
-  CHK_FEW = 27,       // few-token MoE layer: plan, hidden rows, outputs
+  CHK_NORM = 26,      // layer norm: rows, partial rows of the weight gradients
+  CHK_FEW = 27,       // few-token MoE layer: plan, records, hidden rows, outputs
   CHK_LORA = 28,      // adapters: partial sums and outputs
 };
 #ifdef FP8Q_CHECKS
@@ -69,6 +69,10 @@ __device__ __forceinline__ bool chk(int64_t i, int64_t n, uint32_t site) {
 #else
 __device__ __forceinline__ constexpr bool chk(int64_t, int64_t, uint32_t) { return true; }
 #endif
+// Elements from the first to the last of `rows` rows of `cols` that lie `ld` apart.
+__device__ __forceinline__ constexpr int64_t rows_extent(int64_t rows, int64_t cols, int64_t ld) {
+  return (rows - 1) * ld + cols;
+}
 
 // ---------------------------------------------------------------------------
 // Clock record of the GEMM kernels: each CTA adds its SM-clock cycles

@@ -377,7 +377,7 @@ fp8q_status fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x
   fp8q::LayerNormBwdArgs a{};
   a.dy = dy; a.x = x; a.M = M; a.lddy = lddy; a.ldx = ldx; a.N = static_cast<int>(N);
   a.gamma = gamma; a.mean = mean; a.rstd = rstd; a.dx = dx; a.lddx = lddx;
-  a.partial = grads ? workspace : nullptr;
+  a.partial = grads ? workspace : nullptr; a.partial_len = workspace_len;
   const NormShape sh = norm_shape(N, kNormBwdOneVec);
   const int64_t grid = norm_bwd_blocks(M, N, elem_size(x_dtype));
   if (x_dtype == FP8Q_OUT_BF16) {
@@ -482,7 +482,7 @@ fp8q_status fp8q_lora_apply(const void* x, int64_t T, int64_t K, int64_t ldx, co
   g.rows = rows; g.offsets = group_offsets;
   g.a = static_cast<const __nv_bfloat16*>(a); g.b = static_cast<const __nv_bfloat16*>(b); g.scaling = scaling;
   g.base = base; g.ldb = ldb; g.out = out; g.ldo = ldo;
-  g.v = workspace; g.slices = sh.slices;
+  g.v = workspace; g.v_len = workspace_len; g.slices = sh.slices;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (adapters > 0) {
     if (sh.many)

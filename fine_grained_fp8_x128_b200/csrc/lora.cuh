@@ -43,6 +43,7 @@ struct LoraArgs {
   void* out;
   int64_t ldo;
   float* v;                       // [slices][T][r]
+  int64_t v_len;                  // elements there
   int slices;
   int col_units;                  // units of 256 columns an item of the expansion takes
 };
@@ -333,10 +334,10 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraArg
         const int col = 8 * j + 2 * t + c;
         const int rank = w.rank0 + 16 * m + g;
         const int64_t pos = w.first + col;
-        if (col < w.count && chk(pos, a.T, CHK_LORA)) {
-          float* dst = a.v + (w.slice * a.T + pos) * a.r + rank;
-          if (rank < a.r) dst[0] = lo[c];
-          if (rank + 8 < a.r) dst[8] = hi[c];
+        if (col < w.count) {
+          const int64_t at = (w.slice * a.T + pos) * a.r + rank;
+          if (rank < a.r && chk(at, a.v_len, CHK_LORA)) a.v[at] = lo[c];
+          if (rank + 8 < a.r && chk(at + 8, a.v_len, CHK_LORA)) a.v[at + 8] = hi[c];
         }
       }
     }
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(32 * WARPS) lora_expand_kernel(const LoraArgs 
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (mine < a.N && live[m][h] && chk(mine + 7, a.ldo, CHK_LORA)) {
+          if (mine < a.N && live[m][h] &&
+              chk(p_out[m][h] - static_cast<const T*>(a.out) + 7, rows_extent(a.T, a.N, a.ldo), CHK_LORA)) {
             Raw8<T> base;
 #pragma unroll
             for (int w = 0; w < kWords; ++w) base.w[w] = u4[(KQ * 4 + (2 * m + h) * kWords + w) * 32];
@@ -615,7 +617,7 @@ __device__ __forceinline__ void lora_few_units(const LoraArgs& a, int group, boo
 #pragma unroll
     for (int c = 0; c < TC; ++c) {
       const int64_t tok = tokens[c];
-      if (!mine || tok < 0 || !chk(col + 1, a.ldo, CHK_LORA)) continue;
+      if (!mine || tok < 0 || !chk(tok * a.ldo + col + 1, rows_extent(a.T, a.N, a.ldo), CHK_LORA)) continue;
       const float2 d = adapted ? *reinterpret_cast<const float2*>(&sums[c][2 * lane]) : f2(0.0f);
       Pair* out = reinterpret_cast<Pair*>(static_cast<T*>(a.out) + tok * a.ldo + col);
       if constexpr (sizeof(T) == 4) {

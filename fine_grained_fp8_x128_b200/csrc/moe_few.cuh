@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(1024) few_plan_kernel(const FewArgs a) {
     const int t = item / chunks, kb = item - t * chunks;
     const uint2 r = *reinterpret_cast<const uint2*>(a.x + t * a.ldx + kb * 128 + 4 * lane);
     const float f[4] = {bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y)};
-    few_record<false>(f, few_at<uint8_t>(a, a.l.xr) + static_cast<int64_t>(item) * kFewRecord, lane);
+    const int64_t at = a.l.xr + static_cast<int64_t>(item) * kFewRecord;
+    if (chk(at + kFewRecord - 1, a.l.hid, CHK_FEW)) few_record<false>(f, few_at<uint8_t>(a, at), lane);
     return;
   }
   __shared__ int count[kFewMaxExperts], start[kFewMaxExperts];
@@ -525,12 +526,14 @@ few_weights_kernel(const __grid_constant__ CUtensorMap map_lo, const __grid_cons
         const int at = start + col;
         if (MODE == kFewGated) {
           const float h = lo[c] / (1.0f + expf(-lo[c])) * hi[c];
-          if (chk(at, a.l.max_positions, CHK_FEW))
-            few_at<float>(a, a.l.hid)[static_cast<int64_t>(at) * N + row0 + 8 * m + g] = h;
+          const int64_t to = static_cast<int64_t>(at) * N + row0 + 8 * m + g;
+          if (chk(to, a.l.max_positions * a.I, CHK_FEW)) few_at<float>(a, a.l.hid)[to] = h;
         } else {
           const int64_t row = MODE == kFewDown ? entry[at] : at;
-          float* dst = few_at<float>(a, MODE == kFewDown ? a.l.yp : a.l.hid) + row * N + row0 + 16 * m + g;
-          if (chk(row, MODE == kFewDown ? a.T * a.k : a.l.max_positions, CHK_FEW)) {
+          const int64_t to = row * N + row0 + 16 * m + g;
+          float* dst = few_at<float>(a, MODE == kFewDown ? a.l.yp : a.l.hid) + to;
+          const int64_t extent = (MODE == kFewDown ? static_cast<int64_t>(a.T) * a.k : a.l.max_positions) * N;
+          if (chk(to, extent, CHK_FEW) && chk(to + 8, extent, CHK_FEW)) {
             dst[0] = lo[c];
             dst[8] = hi[c];
           }
@@ -555,7 +558,8 @@ __global__ void __launch_bounds__(kFewThreads) few_hidden_kernel(const FewArgs a
     const float4 v = *reinterpret_cast<const float4*>(few_at<const float>(a, a.l.hid) + static_cast<int64_t>(item) * 128 +
                                                       4 * lane);
     const float f[4] = {v.x, v.y, v.z, v.w};
-    few_record<true>(f, few_at<uint8_t>(a, a.l.hr) + static_cast<int64_t>(item) * kFewHiddenRecord, lane);
+    const int64_t at = a.l.hr + static_cast<int64_t>(item) * kFewHiddenRecord;
+    if (chk(at + kFewHiddenRecord - 1, a.l.yp, CHK_FEW)) few_record<true>(f, few_at<uint8_t>(a, at), lane);
   }
 }
 
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(64) few_combine_kernel(const FewArgs a) {
   }
   Raw8<T> o;
   pack8(o, s);
-  if (chk(n + 7, a.ldy, CHK_FEW)) store8(static_cast<T*>(a.y) + t * a.ldy + n, o, 8);
+  if (chk(t * a.ldy + n + 7, rows_extent(a.T, a.H, a.ldy), CHK_FEW)) store8(static_cast<T*>(a.y) + t * a.ldy + n, o, 8);
 }
 
 }  // namespace fp8q

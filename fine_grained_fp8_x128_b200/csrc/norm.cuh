@@ -319,7 +319,8 @@ layer_norm_kernel(const LayerNormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean[r]) * rstd[r], ga[j], be[j]);
         const bool live = row0 + r < a.M;
-        if (a.y != nullptr && live && valid > 0 && chk(8 * static_cast<int64_t>(v) + valid - 1, a.ldy, CHK_NORM)) {
+        if (a.y != nullptr && live && valid > 0 &&
+            chk((row0 + r) * a.ldy + 8 * v + valid - 1, rows_extent(a.M, N, a.ldy), CHK_NORM)) {
           Raw8<T> o;
           pack8(o, f);
           store8(static_cast<T*>(a.y) + (row0 + r) * a.ldy + 8 * static_cast<int64_t>(v), o, valid);
@@ -342,9 +343,10 @@ layer_norm_kernel(const LayerNormArgs a) {
             uint2 o;
             o.x = (c[0] | (c[1] << 16)) ^ kFlipSigns;
             o.y = (c[2] | (c[3] << 16)) ^ kFlipSigns;
-            if (chk(8 * static_cast<int64_t>(v) + 7, a.ldq, CHK_Q1))
+            if (chk((row0 + r) * a.ldq + 8 * v + 7, rows_extent(a.M, N, a.ldq), CHK_Q1))
               *reinterpret_cast<uint2*>(a.q + (row0 + r) * a.ldq + 8 * static_cast<int64_t>(v)) = o;
-            if ((lane & 15) == 0 && chk(row0 + r, a.ld_sf, CHK_Q1_SF)) a.sf[(v >> 4) * a.ld_sf + row0 + r] = s;
+            if ((lane & 15) == 0 && chk((v >> 4) * a.ld_sf + row0 + r, rows_extent(N / 128, a.M, a.ld_sf), CHK_Q1_SF))
+              a.sf[(v >> 4) * a.ld_sf + row0 + r] = s;
           }
         }
       }
@@ -593,7 +595,8 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
           unpack8(raw, f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) f[j] = ffma2(fmul2(fadd2(f[j], m), k), ga[i][j], be[i][j]);
-          if (a.y != nullptr && c.mine[i] && live && chk(8 * c.vec(i) + 7, a.ldy, CHK_NORM)) {
+          if (a.y != nullptr && c.mine[i] && live &&
+              chk((row0 + r) * a.ldy + 8 * c.vec(i) + 7, rows_extent(a.M, a.N, a.ldy), CHK_NORM)) {
             Raw8<T> o;
             pack8(o, f);
             store8(static_cast<T*>(a.y) + (row0 + r) * a.ldy + 8 * c.vec(i), o, 8);
@@ -618,7 +621,8 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
         const float s_l = tile_scale(m);
         const float nr_l = -__frcp_rn(s_l);
         const int64_t own = row0 + r0 + (up ? 1 : 0);
-        if ((lane & 3) == 0 && (up2 ? c.mine[1] : c.mine[0]) && own < a.M && chk(own, a.ld_sf, CHK_Q1_SF))
+        if ((lane & 3) == 0 && (up2 ? c.mine[1] : c.mine[0]) && own < a.M &&
+            chk((c.vec(up2 ? 1 : 0) >> 4) * a.ld_sf + own, rows_extent(a.N / 128, a.M, a.ld_sf), CHK_Q1_SF))
           a.sf[(c.vec(up2 ? 1 : 0) >> 4) * a.ld_sf + own] = s_l;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -634,7 +638,8 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
             uint2 o;
             o.x = (q[0] | (q[1] << 16)) ^ kFlipSigns;
             o.y = (q[2] | (q[3] << 16)) ^ kFlipSigns;
-            if (c.mine[i] && row0 + r0 + u < a.M && chk(8 * c.vec(i) + 7, a.ldq, CHK_Q1))
+            if (c.mine[i] && row0 + r0 + u < a.M &&
+                chk((row0 + r0 + u) * a.ldq + 8 * c.vec(i) + 7, rows_extent(a.M, a.N, a.ldq), CHK_Q1))
               *reinterpret_cast<uint2*>(a.q + (row0 + r0 + u) * a.ldq + 8 * c.vec(i)) = o;
           }
       }
@@ -665,6 +670,7 @@ struct LayerNormBwdArgs {
   void* dx;             // may be null
   int64_t lddx;
   float* partial;       // [gridDim.x][2][N]; null: no weight gradients
+  int64_t partial_len;  // elements there
 };
 
 template <typename T, typename W, int VPT, bool kWarpRow>
@@ -760,7 +766,8 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
             const float xh = (fx[j] - mean[r]) * rstd[r];
             fd[j] = rstd[r] * (fmaf(fd[j], ga[j], -c1[r]) - xh * c2[r]);
           }
-          if (row0 + r < a.M && valid > 0 && chk(8 * static_cast<int64_t>(v) + valid - 1, a.lddx, CHK_NORM)) {
+          if (row0 + r < a.M && valid > 0 &&
+              chk((row0 + r) * a.lddx + 8 * v + valid - 1, rows_extent(a.M, N, a.lddx), CHK_NORM)) {
             Raw8<T> o;
             pack8(o, fd);
             store8(static_cast<T*>(a.dx) + (row0 + r) * a.lddx + 8 * static_cast<int64_t>(v), o, valid);
@@ -788,7 +795,7 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kNormWarpRowThreads / 32; ++w) s += cols[w][c];
-        out[which * N + c] = s;
+        if (chk(out - a.partial + which * N + c, a.partial_len, CHK_NORM)) out[which * N + c] = s;
       }
     }
   } else {
@@ -797,7 +804,7 @@ layer_norm_bwd_kernel(const LayerNormBwdArgs a) {
       const int v = i * nt + t;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (8 * v + j < N) {
+        if (8 * v + j < N && chk(out - a.partial + N + 8 * v + j, a.partial_len, CHK_NORM)) {
           out[8 * v + j] = dga[i][j];
           out[N + 8 * v + j] = dbe[i][j];
         }
@@ -939,7 +946,7 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
             const float2 xh = fmul2(fadd2(x[j], mean[r]), rstd[r]);
             d[j] = fmul2(rstd[r], ffma2(xh, c2, ffma2(d[j], ga[i][j], c1)));
           }
-          if (c.mine[i] && live && chk(8 * c.vec(i) + 7, a.lddx, CHK_NORM)) {
+          if (c.mine[i] && live && chk((row0 + r) * a.lddx + 8 * c.vec(i) + 7, rows_extent(a.M, a.N, a.lddx), CHK_NORM)) {
             Raw8<T> o;
             pack8(o, d);
             store8(static_cast<T*>(a.dx) + (row0 + r) * a.lddx + 8 * c.vec(i), o, 8);
@@ -958,6 +965,7 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_bwd_stream_k
     float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.N + 8 * c.vec(i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (!chk(out - a.partial + a.N + 2 * j + 1, a.partial_len, CHK_NORM)) continue;
       *reinterpret_cast<float2*>(out + 2 * j) = dga[i][j];
       *reinterpret_cast<float2*>(out + a.N + 2 * j) = dbe[i][j];
     }
