@@ -202,7 +202,9 @@ inline bool few_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) 
 // How the adapters' shrink is split: whether the groups hold more than eight
 // tokens on average (blocks of 32 tokens, else of 8), and the K slices that
 // give every SM work when blocks are few.  A function of the sizes alone (the
-// group bounds are on the device).
+// group bounds are on the device).  Skewed groups do not turn the choice around: 256 tokens of 32
+// adapters of rank 64 (blocks of 8), even, half of them on one adapter and all on one, take 33, 47 and 39 us
+// beside 7168 -> 18432 BF16, 257 tokens (blocks of 32) 35, 45 and 45.
 struct LoraShape {
   bool many;
   int ranks;        // an item's ranks: 16, 32 or 64
@@ -291,7 +293,9 @@ fp8q_status lora_expand(const fp8q::LoraArgs& a, DeviceInfo* dev, cudaStream_t s
   const bool after = a.adapters > 0;
   // Few short rows of B a token: FP32 FMAs.  The whole call beside 7168 -> 18432 BF16 with 64 adapters, FMAs and matrix
   // instructions (us): 64 tokens of rank 8 19.1, 25.1, rank 16 22.4, 26.3, rank 32 33.0, 31.5; 128 tokens of rank 16 33.4,
-  // 27.9; 300 tokens of 128 adapters of rank 16 67, 47.
+  // 27.9; 300 tokens of 128 adapters of rank 16 67, 47.  The groups' average decides; on skewed groups the FMAs, which read
+  // a popular adapter's B once for every two tokens (from L2), stay ahead: 64 tokens of 64 adapters of rank 16, half of
+  // them on one adapter and all on one, 18.4 and 17.0, on matrix instructions (65 tokens) 35.3 and 33.8.
   if (a.r <= fp8q::kLoraFewRank && a.T <= a.groups) return lora_expand_few<T>(a, after, dev, s);
   if (a.r <= 32) return launch_lora_expand<T, 1, 2, 2, 16>(a, after, dev, s);
   if (a.r <= 64) return launch_lora_expand<T, 2, kF32 ? 1 : 2, 2, 16>(a, after, dev, s);

@@ -45,7 +45,7 @@ struct LoraArgs {
   float* v;                       // [slices][T][r]
   int64_t v_len;                  // elements there
   int slices;
-  int col_units;                  // units of 256 columns an item of the expansion takes
+  int col_units;                  // an item of the expansion's units, which are 32 columns a warp, for a token a group 64
 };
 
 // The groups' token ranges and the running count of their blocks of `tile`

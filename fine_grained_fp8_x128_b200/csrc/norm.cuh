@@ -1,8 +1,10 @@
 // Layer norm in front of an FP8 projection: forward (into x's type and/or into
 // the projection's 1x128 E4M3 tiles) and backward (input, weight and bias
-// gradients).  Both are HBM-bound streams: each element of the inputs is read
-// once into registers, every sum over a row is formed from registers, and the
-// outputs leave in the same pass.
+// gradients).  Each element of the inputs is read from HBM once, and the outputs
+// leave in the same pass.  The row kernels, for short calls, hold a pair of rows
+// in registers; the streams, for many rows, hold them in a ring in shared memory
+// and read it twice, for the sums and for the outputs.  By its bytes either is
+// HBM's work; what bounds the streams stands there.
 //
 //   mu = sum x / N,  v = sum (x - mu)^2 / N,  r = 1 / sqrt(v + eps)
 //   xh = (x - mu) r,  y = xh gamma + beta
@@ -219,7 +221,7 @@ layer_norm_kernel(const LayerNormArgs a) {
   const int64_t group = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kNormWarpRowThreads / 32) + warp : blockIdx.x;
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (kWarpRow ? kNormWarpRowThreads / 32 : 1);
   const int N = a.N;
-  // true divisions by the counts: a row of one value has exactly that mean and no deviations
+  // true divisions by the counts: a row of one value has exactly that mean and no deviations where its sums are exact
   const float n_f = static_cast<float>(N);
   const float nw_f = static_cast<float>(max(norm_warp_count<VPT>(N, kWarpRow ? 0 : warp, warps), 1));
   int parity = 0;
@@ -362,15 +364,18 @@ layer_norm_kernel(const LayerNormArgs a) {
 // columns' gradients stay in registers for all rows of the block; the rows are
 // read from the ring twice, for the sums and for the outputs, rather than kept in
 // registers, which spilled.  A step's block barrier also tells that the step
-// before is done with its stage.  8192 x 7168 BF16, tiles and backward: 53 and
-// 70 us (and 4.5 for the join), at 34 and 57 % of DRAM: what bounds these kernels
-// is the issue of instructions, at 57 and 53 % of the slots with 14 warps an SM.
+// before is done with its stage.  8192 x 7168 BF16, tiles and backward: 54.5 and
+// 70 us (and 4.5 for the join), at 32 and 55 % of DRAM.  Neither HBM nor the issue
+// of instructions (57 and 53 % of the slots) is full: what bounds these kernels is
+// the latency of a step's two halves and the barrier between them, with 14 warps an SM.
 // Rows kept in registers took 57 and 94 us, one vector a thread (twice the warps
 // for the joins) 59 and 93, two rows a step forward 62; the row kernels, which
 // load a step's rows when it begins, 85 and 126.
 // ---------------------------------------------------------------------------
 constexpr int kNormStages = 3;
-constexpr int kNormStreamThreads = 448;                    // up to 144 registers each
+// Two vectors a thread of rows of up to 7168; the kernels take up to 128 registers.  More threads (512 would fit, for 8192
+// columns) have not been measured.
+constexpr int kNormStreamThreads = 448;
 constexpr int kNormStreamMaxN = 16 * kNormStreamThreads;
 constexpr int kNormFwdRows16 = 4, kNormFwdRows32 = 2;      // rows a step, BF16 and FP32
 constexpr int kNormBwdRows = 2;                            // of x and of dy
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kNormStreamThreads, 1) layer_norm_stream_kerne
       dev += fmaf(count[k] * d, d, p[k].y);
     }
     // as the row kernels round it; the hardware's approximate reciprocal root is off by up to two FP32 steps (and took
-    // 53.3 us where this takes 55 for 8192 x 7168 BF16 into tiles)
+    // 53.3 us where this takes 54.5 for 8192 x 7168 BF16 into tiles)
     const float rstd_l = __frcp_rn(__fsqrt_rn(div_by(row_lanes_sum<R>(dev), c.n, c.inv_n) + a.eps));
     const int64_t row0 = step * R;
     if (c.warp == 0 && lane % kL == 0 && row0 + lane / kL < a.M) {

@@ -617,10 +617,11 @@ fp8q_status fp8q_gemm_mxf8_ue8m0(const void* a, int64_t lda, const uint32_t* sfa
  * Statistics and y are FP32; the variance is the mean square deviation from
  * mu; equal calls give equal bits.  The kernel, and so the order of a row's
  * sums, goes by the sizes: the last FP32 bits of a row's mean and rstd can
- * differ with the number of rows it is given with.  The tiles quantize the FP32 y (rounded once, to E4M3): s =
- * max(fl32(amax / 448), fl32(1e-12)), q = e4m3(y / s).  "Fine-Grained FP8
- * Quantization in DeepSeek", section 2 has the tiles; the pages describe no
- * norm, so the operator's definition is the formula above.
+ * differ with the number of rows it is given with.  The tiles quantize the
+ * FP32 y (rounded once, to E4M3): s = max(fl32(amax / 448), fl32(1e-12)), q =
+ * e4m3(y / s), the quotient within one FP32 step of the rounded one.
+ * "Fine-Grained FP8 Quantization in DeepSeek", section 2 has the tiles; the
+ * pages describe no norm, so the operator's definition is the formula above.
  *   x          : [M][ldx] of x_dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32).
  *   gamma, beta: [N] of param_dtype; NULL stands for ones and zeros.
  *   y          : optional [M][ldy] of x_dtype.  What lies behind a row's N
